@@ -454,6 +454,161 @@ patch_status patch_hybrid_gemm(const patch_packed *Wp, const void *X_bf16, int64
 patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t count, const void *X_bf16,
                                      int64_t M, void *const *Ys, int32_t y_is_fp32, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The operators between the hybrid products of a decoder block: a product
+ * with its epilogue, the gated pair of an MLP, and the norms at the boundary
+ * of two sublayers.  The pages describe the linear layers only ("PATCH",
+ * section 2: every linear layer of the model is one hybrid product); these
+ * calls are what a program runs between them, so that nothing of a block
+ * makes an extra pass over memory.
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+    PATCH_ACT_NONE = 0,      /* v                                                   */
+    PATCH_ACT_RELU = 1,      /* max(v, 0) (NaN stays NaN)                           */
+    PATCH_ACT_GELU = 2,      /* v * Phi(v), Phi the normal distribution (erf form)  */
+    PATCH_ACT_GELU_TANH = 3, /* v/2 * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3)))   */
+    PATCH_ACT_SILU = 4       /* v / (1 + exp(-v))                                   */
+} patch_activation;
+
+/* What follows a product's sums before its one rounding (all in fp32):
+ *     Y[m,n] = residual[m,n] + alpha * act(sum + bias[n])                      */
+typedef struct {
+    const void *bias;          /* [N], or NULL (no bias)                        */
+    const void *residual;      /* [M] rows of N, or NULL                        */
+    int64_t residual_stride;   /* elements between residual rows; 0 = N         */
+    int64_t y_stride;          /* elements between rows of Y; 0 = N             */
+    float alpha;               /* residual scale                                */
+    int32_t activation;        /* patch_activation                              */
+    int32_t bias_is_fp32;      /* else bf16                                     */
+    int32_t residual_is_fp32;  /* else bf16                                     */
+} patch_epilogue;
+
+/*
+ * Hybrid product with an epilogue: Y = residual + alpha * act(X W_eff^T + bias).
+ * The sums are exactly patch_hybrid_gemm's (for FP8 handles with both scales
+ * applied); the epilogue is computed on them in fp32 and the result is
+ * rounded once to Y's type, so no product is stored before it is activated
+ * and added.
+ *
+ *   Wp        handle from any of the pack calls, of the current device.
+ *   X         x_scales NULL: bf16 [M,K] as patch_hybrid_gemm (FP8 handles
+ *             quantise it).  x_scales non-NULL (FP8 handles only): e4m3 codes
+ *             uint8 [M,K] with the fp32 scale of token m at x_scales[m], as
+ *             patch_quantize_fp8 or patch_block_norm writes them; nothing is
+ *             quantised then.  16-byte aligned.
+ *   M         tokens, >= 0 (M == 0 returns PATCH_OK without touching X or Y).
+ *   Y         [M] rows of N, y_stride (>= N) apart: bf16, or fp32
+ *             (y_is_fp32 = 1).  Elements behind a row's N are left as they
+ *             were.  Y may be the residual itself (same address, stride and
+ *             type: the update is then in place); it must not overlap X, the
+ *             bias or the residual in any other way.
+ *   epi       NULL = no bias, no residual, alpha 1, no activation.
+ *
+ * Stream-ordered; never waits for the device; may be captured into a CUDA
+ * graph.  Handles carry scratch: calls on one handle must not run
+ * concurrently (the rule of patch_hybrid_gemm), graphs that hold them
+ * included.  Errors: INVALID_ARG (null or misaligned pointers, a stride below
+ * N, an activation outside the list, x_scales on a handle that is not FP8, a
+ * handle of another device, Y at the residual's address with another stride
+ * or type), OOM, CUDA.
+ */
+patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const float *x_scales,
+                                 int64_t M, void *Y, int32_t y_is_fp32, const patch_epilogue *epi,
+                                 void *stream);
+
+/*
+ * patch_hybrid_linear for `count` (1..8) handles that read the same X, each
+ * with its own Y and epilogue, launched together where
+ * patch_hybrid_gemm_group's products are (one split-K launch at decode token
+ * counts, one two-SM launch in prefill, one quantisation of X).
+ *   epis   host array of count epilogues, or NULL for none.
+ * Every member's arguments are checked before anything is enqueued.  A
+ * handle may appear more than once.  The outputs must not overlap one another.
+ */
+patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t count, const void *X,
+                                       const float *x_scales, int64_t M, void *const *Ys,
+                                       int32_t y_is_fp32, const patch_epilogue *epis, void *stream);
+
+/*
+ * The gated pair of an MLP: Y = act(X W_gate^T + bias_gate) * (X W_up^T + bias_up),
+ * both products' sums as patch_hybrid_gemm's, the rest in fp32, one rounding.
+ *
+ *   Wgate, Wup  handles of the same N and K (any kinds), current device.
+ *   X, x_scales, M  as patch_hybrid_linear (x_scales: both handles FP8).
+ *   Y           [M] rows of N, y_stride (0 = N) apart; must not overlap X.
+ *   bias_gate, bias_up  [N] each or NULL; fp32 when bias_is_fp32, else bf16.
+ *
+ * Notes and errors as patch_hybrid_linear; INVALID_ARG also for handles of
+ * different N or K.
+ */
+patch_status patch_hybrid_gated(const patch_packed *Wgate, const patch_packed *Wup, const void *X,
+                                const float *x_scales, int64_t M, void *Y, int64_t y_stride,
+                                int32_t y_is_fp32, const void *bias_gate, const void *bias_up,
+                                int32_t bias_is_fp32, int32_t activation, void *stream);
+
+typedef enum {
+    PATCH_NORM_NONE = 0,
+    PATCH_NORM_RMS = 1,  /* v / sqrt(mean(v^2) + eps) * weight + bias            */
+    PATCH_NORM_LAYER = 2 /* (v - mean) / sqrt(var + eps) * weight + bias         */
+} patch_norm_kind;
+
+typedef struct {
+    int32_t kind;       /* patch_norm_kind                                       */
+    int32_t is_fp32;    /* weight and bias fp32, else bf16                       */
+    const void *weight; /* [C], or NULL (ones)                                   */
+    const void *bias;   /* [C], or NULL (zeros)                                  */
+    float eps;          /* >= 0                                                  */
+} patch_norm;
+
+typedef enum { PATCH_Z_NONE = 0, PATCH_Z_BF16 = 1, PATCH_Z_FP32 = 2, PATCH_Z_E4M3 = 3 } patch_z_type;
+
+/* Arguments of patch_block_norm.  A stride is in elements between rows; 0
+ * means rows of C one after another. */
+typedef struct {
+    const void *branch;        /* [M] rows of C: the sublayer's output           */
+    int64_t branch_stride;
+    const void *residual;      /* [M] rows of C, or NULL (zeros)                 */
+    int64_t residual_stride;
+    const void *gate;          /* [ceil(M / gate_tokens)] rows of C, or NULL (ones) */
+    int64_t gate_stride;
+    int64_t gate_tokens;       /* consecutive tokens that share a gate row (>= 1):
+                                  1 = a gate per token, >= M = one per channel   */
+    void *h;                   /* [M] rows of C, or NULL (not written)           */
+    int64_t h_stride;
+    void *z;                   /* [M] rows of C, or NULL with z_type NONE        */
+    int64_t z_stride;
+    float *z_scales;           /* [M], z_type E4M3 only                          */
+    patch_norm post, pre;
+    float scale;
+    int32_t branch_is_fp32, residual_is_fp32, gate_is_fp32, h_is_fp32;  /* else bf16 */
+    int32_t z_type;            /* patch_z_type                                   */
+} patch_block_norm_args;
+
+/*
+ * The boundary between two sublayers in one pass over the rows:
+ *     h = residual + scale * gate * norm_post(branch)     (the residual stream)
+ *     z = norm_pre(h)                                     (the next layer's input)
+ * Every step is computed in fp32 from the inputs as stored (z from h before
+ * h is rounded), each output rounded once.  z_type E4M3 writes e4m3 codes
+ * and one scale per token, s = amax |z| / 448 (1 for a zero row),
+ * q = e4m3(z / s), in the form patch_hybrid_linear's x_scales takes; the
+ * codes come from the fp32 values, not from values rounded to bf16 first.
+ *
+ *   M  rows, >= 0 (0 returns PATCH_OK without touching anything).
+ *   C  1 .. 32768, any value (multiples of 8 with 16-byte aligned pointers and
+ *      strides take 16-byte accesses).
+ *
+ * h and z may each be the residual or the branch itself, not both the same one
+ * (same address, stride and type); no other overlap.  Stream-ordered, no
+ * scratch, no allocation.  Errors: INVALID_ARG (null branch, neither h nor z,
+ * a stride below C, unknown kinds or types, eps negative or not a number,
+ * misaligned pointers, z without z_type or z_scales where E4M3, an output at
+ * an input's address with another stride or type), UNSUPPORTED (C above 32768,
+ * not sm_100), CUDA.
+ */
+patch_status patch_block_norm(const patch_block_norm_args *args, int64_t M, int64_t C, void *stream);
+
 /*
  * Failure-detection test hook: while `on` is non-zero, the first CTA of every
  * later patch_hybrid_gemm never loads its first k-step, so that CTA's bounded

@@ -5,8 +5,10 @@ is its thin ctypes binding.  Importing this package does not load the CUDA
 library; the first call does, and fails loudly if it is missing.
 """
 from .patch import (PackedWeight, PatchError, PatchLibraryError, load_library,  # noqa: F401
-                    patch_free, patch_get_status, patch_hybrid_gemm, patch_pack,
-                    patch_score_mask)
+                    patch_block_norm, patch_free, patch_get_status, patch_hybrid_gated,
+                    patch_hybrid_gemm, patch_hybrid_linear, patch_hybrid_linear_group,
+                    patch_pack, patch_score_mask)
 
-__all__ = ["PackedWeight", "PatchError", "PatchLibraryError", "load_library", "patch_free",
-           "patch_get_status", "patch_hybrid_gemm", "patch_pack", "patch_score_mask"]
+__all__ = ["PackedWeight", "PatchError", "PatchLibraryError", "load_library", "patch_block_norm",
+           "patch_free", "patch_get_status", "patch_hybrid_gated", "patch_hybrid_gemm",
+           "patch_hybrid_linear", "patch_hybrid_linear_group", "patch_pack", "patch_score_mask"]

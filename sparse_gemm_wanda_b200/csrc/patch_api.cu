@@ -423,6 +423,7 @@ static void preload_gemm_kernels() {
     patchk::preload_duo_fp8_kernels();
     patchk::preload_fp8_quantize_kernels();
     patchk::preload_pack_kernels();
+    patchk::preload_epilogue_kernels();
     if (named) done.insert(id);
 }
 
@@ -934,9 +935,20 @@ static patchk::Fp8Launch fp8_launch(const patch_packed *Wp, const uint8_t *xq, c
     return g;
 }
 
-static patch_status fp8_gemm(const patch_packed *Wp, const void *X_bf16, int64_t M, void *Y,
+// x_scales non-null: X holds e4m3 codes already and nothing is quantised.
+static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
                              int32_t y_is_fp32, cudaStream_t stream) {
     const int64_t K = Wp->shp.K;
+    const int force = g_test_kernel.load(std::memory_order_relaxed);
+    // decode token counts: the split-K kernel on the e4m3 codes, the weights
+    // read once over every SM; the fix-up applies the row and token scales
+    const bool split = M <= patchk::kDecodeMaxM && Wp->dec_nchunks > 0 && force == 0;
+    auto product = [&](const uint8_t *xq, const float *sx) {
+        if (!split) return patchk::launch_fp8_gemm(fp8_launch(Wp, xq, sx, M, Y, y_is_fp32), stream);
+        const patchk::GemmLaunch g = fp8_split_launch(Wp, xq, sx, M, Y, y_is_fp32);
+        return patchk::launch_decode_f8(&g, 1, stream);
+    };
+    if (x_scales) return from_cuda(product(static_cast<const uint8_t *>(X), x_scales));
     // the activations' codes and token scales
     const size_t off_sx = round_up(static_cast<size_t>(M * K), 256);
     const size_t bytes = off_sx + sizeof(float) * static_cast<size_t>(M);
@@ -949,16 +961,8 @@ static patch_status fp8_gemm(const patch_packed *Wp, const void *X_bf16, int64_t
         e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes, Wp->pool, stream);
     if (e != cudaSuccess) return from_cuda(e);
     float *sx = reinterpret_cast<float *>(ws + off_sx);
-    e = patchk::launch_fp8_quantize_rows(X_bf16, M, K, ws, sx, stream);
-    const int force = g_test_kernel.load(std::memory_order_relaxed);
-    if (e == cudaSuccess && M <= patchk::kDecodeMaxM && Wp->dec_nchunks > 0 && force == 0) {
-        // decode token counts: the split-K kernel on the e4m3 codes, the weights
-        // read once over every SM; the fix-up applies the row and token scales
-        const patchk::GemmLaunch g = fp8_split_launch(Wp, ws, sx, M, Y, y_is_fp32);
-        e = patchk::launch_decode_f8(&g, 1, stream);
-    } else if (e == cudaSuccess) {
-        e = patchk::launch_fp8_gemm(fp8_launch(Wp, ws, sx, M, Y, y_is_fp32), stream);
-    }
+    e = patchk::launch_fp8_quantize_rows(X, M, K, ws, sx, stream);
+    if (e == cudaSuccess) e = product(ws, sx);
     const cudaError_t e2 = own ? cudaSuccess : cudaFreeAsync(ws, stream);
     return from_cuda(e != cudaSuccess ? e : e2);
 }
@@ -1000,6 +1004,13 @@ static patchk::GemmLaunch gemm_launch(const patch_packed *Wp, const void *X_bf16
     return g;
 }
 
+static patch_status product_one(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
+                                int32_t y_is_fp32, cudaStream_t stream) {
+    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, stream);
+    const patchk::GemmLaunch g = gemm_launch(Wp, X, M, Y, y_is_fp32);
+    return from_cuda(patchk::launch_hybrid_gemm(g, stream));
+}
+
 patch_status patch_hybrid_gemm(const patch_packed *Wp, const void *X_bf16, int64_t M, void *Y,
                                int32_t y_is_fp32, void *stream_v) {
     if (!Wp || M < 0) return PATCH_ERR_INVALID_ARG;
@@ -1008,25 +1019,15 @@ patch_status patch_hybrid_gemm(const patch_packed *Wp, const void *X_bf16, int64
     if (!aligned16(X_bf16) || !aligned16(Y)) return PATCH_ERR_INVALID_ARG;
     if (y_is_fp32 != 0 && y_is_fp32 != 1) return PATCH_ERR_INVALID_ARG;
     if (M > (int64_t(1) << 31)) return PATCH_ERR_INVALID_ARG;
-    if (Wp->pattern == 8) return fp8_gemm(Wp, X_bf16, M, Y, y_is_fp32, static_cast<cudaStream_t>(stream_v));
-    const patchk::GemmLaunch g = gemm_launch(Wp, X_bf16, M, Y, y_is_fp32);
-    return from_cuda(patchk::launch_hybrid_gemm(g, static_cast<cudaStream_t>(stream_v)));
+    return product_one(Wp, X_bf16, nullptr, M, Y, y_is_fp32, static_cast<cudaStream_t>(stream_v));
 }
 
-patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t count, const void *X_bf16,
-                                     int64_t M, void *const *Ys, int32_t y_is_fp32, void *stream_v) {
-    if (!Wps || !Ys || count < 1 || count > patchk::kDecMaxGroup || M < 0) return PATCH_ERR_INVALID_ARG;
-    for (int i = 0; i < count; ++i)
-        if (!Wps[i]) return PATCH_ERR_INVALID_ARG;
-    if (M == 0) return PATCH_OK;
-    if (!X_bf16 || !aligned16(X_bf16)) return PATCH_ERR_INVALID_ARG;
-    for (int i = 0; i < count; ++i)
-        if (!Ys[i] || !aligned16(Ys[i])) return PATCH_ERR_INVALID_ARG;
-    if (y_is_fp32 != 0 && y_is_fp32 != 1) return PATCH_ERR_INVALID_ARG;
-    if (M > (int64_t(1) << 31)) return PATCH_ERR_INVALID_ARG;
+// The products of handles that read the same X (checked by the caller), in
+// one launch where the library can (see patch_hybrid_gemm_group).
+static patch_status products(const patch_packed *const *Wps, int32_t count, const void *X, const float *x_scales,
+                             int64_t M, void *const *Ys, int32_t y_is_fp32, cudaStream_t stream) {
     const int64_t K = Wps[0]->shp.K;
     const int force = g_test_kernel.load(std::memory_order_relaxed);
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     // FP8 handles: X is quantised once (into the first handle's scratch) and
     // the group's products run as one split-K launch on the codes
     bool f8_group = count > 1 && M <= kFp8ScratchRows && M <= patchk::kDecodeMaxM && force == 0;
@@ -1034,10 +1035,16 @@ patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t cou
         f8_group = Wps[i]->pattern == 8 && Wps[i]->shp.K == K && Wps[i]->dec_nchunks > 0 &&
                    Wps[i]->num_sms == Wps[0]->num_sms && Wps[0]->fp8_xscratch;
     if (f8_group) {
-        uint8_t *xq = Wps[0]->fp8_xscratch;
-        float *sx = reinterpret_cast<float *>(xq + round_up(static_cast<size_t>(M * K), 256));
-        cudaError_t e = patchk::launch_fp8_quantize_rows(X_bf16, M, K, xq, sx, stream);
-        if (e != cudaSuccess) return from_cuda(e);
+        const uint8_t *xq = static_cast<const uint8_t *>(X);
+        const float *sx = x_scales;
+        if (!x_scales) {
+            uint8_t *q = Wps[0]->fp8_xscratch;
+            float *s = reinterpret_cast<float *>(q + round_up(static_cast<size_t>(M * K), 256));
+            const cudaError_t e = patchk::launch_fp8_quantize_rows(X, M, K, q, s, stream);
+            if (e != cudaSuccess) return from_cuda(e);
+            xq = q;
+            sx = s;
+        }
         patchk::GemmLaunch gs[patchk::kDecMaxGroup];
         for (int i = 0; i < count; ++i) gs[i] = fp8_split_launch(Wps[i], xq, sx, M, Ys[i], y_is_fp32);
         return from_cuda(patchk::launch_decode_f8(gs, count, stream));
@@ -1065,6 +1072,12 @@ patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t cou
         patchk::DuoFp8Plan dp{};
         if (ok) dp = patchk::plan_duo_fp8(sum_n, M, Wps[0]->num_sms, all_sparse);
         if (ok && dp.bn > 0 && (force == 3 || dp.cost <= own)) {
+            auto launch = [&](const uint8_t *xq, const float *sx) {
+                patchk::Fp8Launch gs[patchk::kDecMaxGroup];
+                for (int i = 0; i < count; ++i) gs[i] = fp8_launch(Wps[i], xq, sx, M, Ys[i], y_is_fp32);
+                return patchk::launch_duo_fp8_group(gs, count, dp, stream);
+            };
+            if (x_scales) return from_cuda(launch(static_cast<const uint8_t *>(X), x_scales));
             const size_t off_sx = round_up(static_cast<size_t>(M * K), 256);
             uint8_t *ws = nullptr;
             cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws),
@@ -1072,12 +1085,8 @@ patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t cou
                                                     Wps[0]->pool, stream);
             if (e != cudaSuccess) return from_cuda(e);
             float *sx = reinterpret_cast<float *>(ws + off_sx);
-            e = patchk::launch_fp8_quantize_rows(X_bf16, M, K, ws, sx, stream);
-            if (e == cudaSuccess) {
-                patchk::Fp8Launch gs[patchk::kDecMaxGroup];
-                for (int i = 0; i < count; ++i) gs[i] = fp8_launch(Wps[i], ws, sx, M, Ys[i], y_is_fp32);
-                e = patchk::launch_duo_fp8_group(gs, count, dp, stream);
-            }
+            e = patchk::launch_fp8_quantize_rows(X, M, K, ws, sx, stream);
+            if (e == cudaSuccess) e = launch(ws, sx);
             const cudaError_t e2 = cudaFreeAsync(ws, stream);
             return from_cuda(e != cudaSuccess ? e : e2);
         }
@@ -1090,7 +1099,7 @@ patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t cou
         for (int i = 0; i < count && same; ++i) same = Wps[i]->shp.K == K;
         if (same) {
             patchk::GemmLaunch gs[patchk::kDecMaxGroup];
-            for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X_bf16, M, Ys[i], y_is_fp32);
+            for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X, M, Ys[i], y_is_fp32);
             patchk::DuoPlan dp;
             if (patchk::plan_hybrid_group(gs, count, &dp)) return from_cuda(patchk::launch_duo_group(gs, count, dp, stream));
         }
@@ -1101,14 +1110,208 @@ patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t cou
     if (!one_launch) {
         // the products one after another on the stream (the same results)
         for (int i = 0; i < count; ++i) {
-            const patch_status st = patch_hybrid_gemm(Wps[i], X_bf16, M, Ys[i], y_is_fp32, stream_v);
+            const patch_status st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, stream);
             if (st != PATCH_OK) return st;
         }
         return PATCH_OK;
     }
     patchk::GemmLaunch gs[patchk::kDecMaxGroup];
-    for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X_bf16, M, Ys[i], y_is_fp32);
+    for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X, M, Ys[i], y_is_fp32);
     return from_cuda(patchk::launch_decode_group(gs, count, stream));
+}
+
+patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t count, const void *X_bf16,
+                                     int64_t M, void *const *Ys, int32_t y_is_fp32, void *stream_v) {
+    if (!Wps || !Ys || count < 1 || count > patchk::kDecMaxGroup || M < 0) return PATCH_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i)
+        if (!Wps[i]) return PATCH_ERR_INVALID_ARG;
+    if (M == 0) return PATCH_OK;
+    if (!X_bf16 || !aligned16(X_bf16)) return PATCH_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i)
+        if (!Ys[i] || !aligned16(Ys[i])) return PATCH_ERR_INVALID_ARG;
+    if (y_is_fp32 != 0 && y_is_fp32 != 1) return PATCH_ERR_INVALID_ARG;
+    if (M > (int64_t(1) << 31)) return PATCH_ERR_INVALID_ARG;
+    return products(Wps, count, X_bf16, nullptr, M, Ys, y_is_fp32, static_cast<cudaStream_t>(stream_v));
+}
+
+// -------------------------------------------- products with an epilogue
+static bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+static size_t real_bytes(int32_t is_fp32) { return is_fp32 ? 4 : 2; }
+static bool flag_ok(int32_t v) { return v == 0 || v == 1; }
+
+// X, the handles and M of the calls below; the handles' device must be current.
+static patch_status check_products(const patch_packed *const *Wps, int32_t count, const void *X,
+                                   const float *x_scales, int64_t M) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PATCH_ERR_CUDA;
+    for (int i = 0; i < count; ++i) {
+        if (!Wps[i] || Wps[i]->device != dev || Wps[i]->shp.K != Wps[0]->shp.K) return PATCH_ERR_INVALID_ARG;
+        if (x_scales && Wps[i]->pattern != 8) return PATCH_ERR_INVALID_ARG;
+    }
+    if (M < 0 || M > INT32_MAX) return PATCH_ERR_INVALID_ARG;
+    if (M > 0 && (!X || !aligned16(X) || !aligned_to(x_scales, 4))) return PATCH_ERR_INVALID_ARG;
+    return PATCH_OK;
+}
+
+// One member's epilogue and output checked and resolved into `out`.
+static patch_status check_epilogue(const patch_epilogue *epi, int64_t N, int64_t M, const void *Y, int32_t y_is_fp32,
+                                   patchk::Epilogue *out) {
+    const patch_epilogue none = {nullptr, nullptr, 0, 0, 1.0f, PATCH_ACT_NONE, 0, 0};
+    const patch_epilogue &e = epi ? *epi : none;
+    if (e.activation < PATCH_ACT_NONE || e.activation > PATCH_ACT_SILU) return PATCH_ERR_INVALID_ARG;
+    if (!flag_ok(e.bias_is_fp32) || !flag_ok(e.residual_is_fp32) || !flag_ok(y_is_fp32)) return PATCH_ERR_INVALID_ARG;
+    const int64_t ldy = e.y_stride ? e.y_stride : N, ldr = e.residual_stride ? e.residual_stride : N;
+    if (ldy < N || ldr < N) return PATCH_ERR_INVALID_ARG;
+    if (!aligned_to(e.bias, real_bytes(e.bias_is_fp32)) || !aligned_to(e.residual, real_bytes(e.residual_is_fp32)) ||
+        !aligned_to(Y, real_bytes(y_is_fp32)))
+        return PATCH_ERR_INVALID_ARG;
+    if (M > 0 && !Y) return PATCH_ERR_INVALID_ARG;
+    // in place: every element is read and written by one thread, so the two must coincide
+    if (Y && Y == e.residual && (ldy != ldr || y_is_fp32 != e.residual_is_fp32)) return PATCH_ERR_INVALID_ARG;
+    *out = patchk::Epilogue{e.bias, nullptr, e.residual, ldr, ldy, e.alpha, e.activation, e.bias_is_fp32,
+                            e.residual_is_fp32};
+    return PATCH_OK;
+}
+
+// fp32 sums of every member in one pool block for the call, [M, N_i] each
+static patch_status sums_of(const patch_packed *const *Wps, int32_t count, const void *X, const float *x_scales,
+                            int64_t M, float **base, float **sums, cudaStream_t stream) {
+    size_t total = 0, off[patchk::kDecMaxGroup];
+    for (int i = 0; i < count; ++i) {
+        off[i] = total;
+        total = round_up(total + sizeof(float) * static_cast<size_t>(M) * static_cast<size_t>(Wps[i]->shp.N), 256);
+    }
+    uint8_t *ws = nullptr;
+    const cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), total, Wps[0]->pool, stream);
+    if (e != cudaSuccess) return from_cuda(e);
+    *base = reinterpret_cast<float *>(ws);
+    void *ys[patchk::kDecMaxGroup];
+    for (int i = 0; i < count; ++i) ys[i] = sums[i] = reinterpret_cast<float *>(ws + off[i]);
+    return products(Wps, count, X, x_scales, M, ys, 1, stream);
+}
+
+patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t count, const void *X,
+                                       const float *x_scales, int64_t M, void *const *Ys, int32_t y_is_fp32,
+                                       const patch_epilogue *epis, void *stream_v) {
+    if (!Wps || !Ys || count < 1 || count > patchk::kDecMaxGroup) return PATCH_ERR_INVALID_ARG;
+    if (!Wps[0]) return PATCH_ERR_INVALID_ARG;
+    patch_status st = check_products(Wps, count, X, x_scales, M);
+    if (st != PATCH_OK) return st;
+    patchk::Epilogue es[patchk::kDecMaxGroup];
+    for (int i = 0; i < count; ++i) {
+        st = check_epilogue(epis ? epis + i : nullptr, Wps[i]->shp.N, M, Ys[i], y_is_fp32, &es[i]);
+        if (st != PATCH_OK) return st;
+    }
+    if (M == 0) return PATCH_OK;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    float *base = nullptr, *sums[patchk::kDecMaxGroup];
+    st = sums_of(Wps, count, X, x_scales, M, &base, sums, stream);
+    for (int i = 0; i < count && st == PATCH_OK; ++i)
+        st = from_cuda(patchk::launch_epilogue(sums[i], nullptr, Ys[i], y_is_fp32, Wps[i]->shp.N, M, es[i], stream));
+    if (base) {
+        const cudaError_t e2 = cudaFreeAsync(base, stream);
+        if (st == PATCH_OK) st = from_cuda(e2);
+    }
+    return st;
+}
+
+patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
+                                 int32_t y_is_fp32, const patch_epilogue *epi, void *stream_v) {
+    return patch_hybrid_linear_group(&Wp, 1, X, x_scales, M, &Y, y_is_fp32, epi, stream_v);
+}
+
+patch_status patch_hybrid_gated(const patch_packed *Wgate, const patch_packed *Wup, const void *X,
+                                const float *x_scales, int64_t M, void *Y, int64_t y_stride, int32_t y_is_fp32,
+                                const void *bias_gate, const void *bias_up, int32_t bias_is_fp32, int32_t activation,
+                                void *stream_v) {
+    if (!Wgate || !Wup || Wgate->shp.N != Wup->shp.N) return PATCH_ERR_INVALID_ARG;
+    const patch_packed *hs[2] = {Wgate, Wup};
+    patch_status st = check_products(hs, 2, X, x_scales, M);
+    if (st != PATCH_OK) return st;
+    const patch_epilogue pe = {bias_gate, nullptr, 0, y_stride, 1.0f, activation, bias_is_fp32, 0};
+    patchk::Epilogue e;
+    st = check_epilogue(&pe, Wgate->shp.N, M, Y, y_is_fp32, &e);
+    if (st != PATCH_OK) return st;
+    if (!aligned_to(bias_up, real_bytes(bias_is_fp32))) return PATCH_ERR_INVALID_ARG;
+    e.bias2 = bias_up;
+    if (M == 0) return PATCH_OK;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    float *base = nullptr, *sums[2];
+    st = sums_of(hs, 2, X, x_scales, M, &base, sums, stream);
+    if (st == PATCH_OK)
+        st = from_cuda(patchk::launch_epilogue(sums[0], sums[1], Y, y_is_fp32, Wgate->shp.N, M, e, stream));
+    if (base) {
+        const cudaError_t e2 = cudaFreeAsync(base, stream);
+        if (st == PATCH_OK) st = from_cuda(e2);
+    }
+    return st;
+}
+
+// ------------------------------------------------------- norms of a block
+static bool norm_ok(const patch_norm &n) {
+    return n.kind >= PATCH_NORM_NONE && n.kind <= PATCH_NORM_LAYER && flag_ok(n.is_fp32) &&
+           (n.kind == PATCH_NORM_NONE || n.eps >= 0.0f) && aligned_to(n.weight, real_bytes(n.is_fp32)) &&
+           aligned_to(n.bias, real_bytes(n.is_fp32));
+}
+
+patch_status patch_block_norm(const patch_block_norm_args *a, int64_t M, int64_t C, void *stream_v) {
+    if (!a || M < 0 || M > INT32_MAX || C < 1) return PATCH_ERR_INVALID_ARG;
+    if (!norm_ok(a->post) || !norm_ok(a->pre)) return PATCH_ERR_INVALID_ARG;
+    if (!flag_ok(a->branch_is_fp32) || !flag_ok(a->residual_is_fp32) || !flag_ok(a->gate_is_fp32) ||
+        !flag_ok(a->h_is_fp32))
+        return PATCH_ERR_INVALID_ARG;
+    if (a->z_type < PATCH_Z_NONE || a->z_type > PATCH_Z_E4M3) return PATCH_ERR_INVALID_ARG;
+    auto stride = [C](int64_t s) { return s ? s : C; };
+    patchk::BlockNormParams p;
+    p.branch_stride = stride(a->branch_stride);
+    p.residual_stride = stride(a->residual_stride);
+    p.gate_stride = stride(a->gate_stride);
+    p.h_stride = stride(a->h_stride);
+    p.z_stride = stride(a->z_stride);
+    if (p.branch_stride < C || p.residual_stride < C || p.gate_stride < C || p.h_stride < C || p.z_stride < C)
+        return PATCH_ERR_INVALID_ARG;
+    if (a->gate && a->gate_tokens < 1) return PATCH_ERR_INVALID_ARG;
+    const bool e4m3 = a->z_type == PATCH_Z_E4M3;
+    if (!aligned_to(a->branch, real_bytes(a->branch_is_fp32)) || !aligned_to(a->residual, real_bytes(a->residual_is_fp32)) ||
+        !aligned_to(a->gate, real_bytes(a->gate_is_fp32)) || !aligned_to(a->h, real_bytes(a->h_is_fp32)) ||
+        (!e4m3 && !aligned_to(a->z, real_bytes(a->z_type == PATCH_Z_FP32))) || !aligned_to(a->z_scales, 4))
+        return PATCH_ERR_INVALID_ARG;
+    // in place: a thread writes the elements it read, so both must coincide
+    const int32_t z_fp32 = a->z_type == PATCH_Z_FP32;
+    auto clash = [](const void *out, int64_t os, int32_t of, const void *in, int64_t is, int32_t inf) {
+        return out && out == in && (os != is || of != inf);
+    };
+    if (clash(a->h, p.h_stride, a->h_is_fp32, a->branch, p.branch_stride, a->branch_is_fp32) ||
+        clash(a->h, p.h_stride, a->h_is_fp32, a->residual, p.residual_stride, a->residual_is_fp32) ||
+        clash(a->z, p.z_stride, e4m3 ? 2 : z_fp32, a->branch, p.branch_stride, a->branch_is_fp32) ||
+        clash(a->z, p.z_stride, e4m3 ? 2 : z_fp32, a->residual, p.residual_stride, a->residual_is_fp32) ||
+        (a->h && a->h == a->z))
+        return PATCH_ERR_INVALID_ARG;
+    if (C > patchk::kNormMaxC) return PATCH_ERR_UNSUPPORTED;
+    if (M == 0) return PATCH_OK;
+    if (!a->branch || (!a->h && a->z_type == PATCH_Z_NONE) || (a->z_type != PATCH_Z_NONE && !a->z) ||
+        (a->z && a->z_type == PATCH_Z_NONE) || (e4m3 && !a->z_scales))
+        return PATCH_ERR_INVALID_ARG;
+    const patch_status st = check_device(nullptr);
+    if (st != PATCH_OK) return st;
+    p.branch = a->branch;
+    p.residual = a->residual;
+    p.gate = a->gate;
+    p.h = a->h;
+    p.z = a->z;
+    p.z_scales = a->z_scales;
+    p.gate_tokens = a->gate ? a->gate_tokens : 1;
+    p.M = M;
+    p.post = patchk::NormSpec{a->post.weight, a->post.bias, a->post.eps, a->post.kind, a->post.is_fp32};
+    p.pre = patchk::NormSpec{a->pre.weight, a->pre.bias, a->pre.eps, a->pre.kind, a->pre.is_fp32};
+    p.scale = a->scale;
+    p.C = static_cast<int>(C);
+    p.branch_fp32 = a->branch_is_fp32;
+    p.residual_fp32 = a->residual_is_fp32;
+    p.gate_fp32 = a->gate_is_fp32;
+    p.h_fp32 = a->h_is_fp32;
+    p.z_type = a->z_type;
+    return from_cuda(patchk::launch_block_norm(p, static_cast<cudaStream_t>(stream_v)));
 }
 
 void patch_free(patch_packed *Wp, void *stream_v) {

@@ -271,6 +271,46 @@ cudaError_t launch_duo_fp8(const Fp8Launch &g, const DuoFp8Plan &plan, cudaStrea
 // their N, with all_sparse only if every matrix is.
 cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Plan &plan, cudaStream_t stream);
 
+// What follows a product's sums (patch_epilogue of include/patch.h, resolved:
+// strides filled in).  The gated pair uses bias (gate), bias2 (up) and act.
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+struct Epilogue {
+    const void *bias;      // [N] or null
+    const void *bias2;     // gated pair: the up product's bias, or null
+    const void *residual;  // [M] rows ldr apart, or null
+    int64_t ldr, ldy;
+    float alpha;
+    int act;
+    int bias_fp32, res_fp32;
+};
+// `up` null: Y = residual + alpha * act(sum + bias); else Y = act(sum + bias)
+// * (up + bias2).  sum and up are [M, N] fp32, N a multiple of 128.
+cudaError_t launch_epilogue(const float *sum, const float *up, void *Y, int y_fp32, int64_t N, int64_t M,
+                            const Epilogue &e, cudaStream_t stream);
+void preload_epilogue_kernels();
+
+// Norms at the boundary of two sublayers (csrc/block_norm.cu); the fields of
+// patch_block_norm_args with the strides filled in.
+enum { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
+enum { kZNone = 0, kZBf16 = 1, kZFp32 = 2, kZE4m3 = 3 };
+constexpr int kNormMaxC = 32768;
+struct NormSpec {
+    const void *weight, *bias;
+    float eps;
+    int kind, fp32;
+};
+struct BlockNormParams {
+    const void *branch, *residual, *gate;
+    void *h, *z;
+    float *z_scales;
+    int64_t branch_stride, residual_stride, gate_stride, gate_tokens, h_stride, z_stride;
+    int64_t M;
+    NormSpec post, pre;
+    float scale;
+    int C, branch_fp32, residual_fp32, gate_fp32, h_fp32, z_type;
+};
+cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream);
+
 // The library's stream-ordered memory pool for the current device (cached
 // memory is kept, not returned to the system between calls).
 cudaError_t device_pool(cudaMemPool_t *pool);

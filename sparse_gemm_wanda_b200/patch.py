@@ -27,7 +27,16 @@ EXPORTS = ("patch_score_mask", "patch_pack", "patch_hybrid_gemm", "patch_free",
            "patch_select_maps_global", "patch_test_stall_first_kstep", "patch_pool_usage",
            "patch_colsq", "patch_colsq_partials", "patch_colsq_fold", "patch_test_prefill_kernel",
            "patch_score_mask_nm", "patch_pack_nm", "patch_pack_fp8", "patch_quantize_fp8",
-           "patch_packed_fp8_scales", "patch_hybrid_gemm_group", "patch_pack_group")
+           "patch_packed_fp8_scales", "patch_hybrid_gemm_group", "patch_pack_group",
+           "patch_hybrid_linear", "patch_hybrid_linear_group", "patch_hybrid_gated",
+           "patch_block_norm")
+
+# patch_activation, patch_norm_kind and patch_z_type of include/patch.h
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+NORMS = {"rms": 1, "layer": 2}
+Z_TYPES = {"bf16": 1, "fp32": 2, "e4m3": 3}
+NORM_MAX_C = 32768
+_REAL = (torch.bfloat16, torch.float32)
 
 
 class PatchLibraryError(RuntimeError):
@@ -50,6 +59,30 @@ class PatchPackedView(ctypes.Structure):
                 ("packed_bytes", ctypes.c_size_t), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("tile_n", ctypes.c_int32), ("tile_k", ctypes.c_int32),
                 ("sparse_ksteps", ctypes.c_int64), ("meta_blocks", ctypes.c_int64)]
+
+
+class PatchEpilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("alpha", ctypes.c_float), ("activation", ctypes.c_int32),
+                ("bias_is_fp32", ctypes.c_int32), ("residual_is_fp32", ctypes.c_int32)]
+
+
+class PatchNorm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("is_fp32", ctypes.c_int32), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class PatchBlockNormArgs(ctypes.Structure):
+    _fields_ = [("branch", ctypes.c_void_p), ("branch_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64),
+                ("gate_tokens", ctypes.c_int64), ("h", ctypes.c_void_p), ("h_stride", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("z_stride", ctypes.c_int64), ("z_scales", ctypes.c_void_p),
+                ("post", PatchNorm), ("pre", PatchNorm), ("scale", ctypes.c_float),
+                ("branch_is_fp32", ctypes.c_int32), ("residual_is_fp32", ctypes.c_int32),
+                ("gate_is_fp32", ctypes.c_int32), ("h_is_fp32", ctypes.c_int32),
+                ("z_type", ctypes.c_int32)]
 
 
 _lib = None
@@ -113,6 +146,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.patch_hybrid_gemm.argtypes = [vp, vp, i64, vp, i32, vp]
     lib.patch_hybrid_gemm_group.argtypes = [ctypes.POINTER(vp), i32, vp, i64, ctypes.POINTER(vp), i32, vp]
     lib.patch_hybrid_gemm_group.restype = ctypes.c_int
+    epi_p = ctypes.POINTER(PatchEpilogue)
+    lib.patch_hybrid_linear.argtypes = [vp, vp, vp, i64, vp, i32, epi_p, vp]
+    lib.patch_hybrid_linear_group.argtypes = [ctypes.POINTER(vp), i32, vp, vp, i64, ctypes.POINTER(vp), i32,
+                                              epi_p, vp]
+    lib.patch_hybrid_gated.argtypes = [vp, vp, vp, vp, i64, vp, i64, i32, vp, vp, i32, i32, vp]
+    lib.patch_block_norm.argtypes = [ctypes.POINTER(PatchBlockNormArgs), i64, i64, vp]
+    for name in ("patch_hybrid_linear", "patch_hybrid_linear_group", "patch_hybrid_gated", "patch_block_norm"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.patch_free.argtypes = [vp, vp]
     lib.patch_free.restype = None
     lib.patch_get_status.argtypes = [vp]
@@ -449,6 +490,232 @@ def patch_hybrid_gemm_group(packed: list, X: torch.Tensor, outs: list | None = N
                                        1 if out_fp32 else 0, _stream(stream))
     _check("patch_hybrid_gemm_group", code)
     return outs
+
+
+class _Launch:
+    """The device, stream and row checks shared by the calls below.
+
+    Every tensor has to be on the current device.  Outputs are allocated for
+    the stream the call runs on, so that the allocator does not hand their
+    memory to other work while the call is still queued."""
+
+    def __init__(self, x: torch.Tensor, name: str, stream):
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        self.device = x.device
+        if x.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+        if stream is not None and stream.device != x.device:
+            raise ValueError(f"the stream is on {stream.device}, {name} on {x.device}")
+        self.torch_stream = stream
+        self.stream = _stream(stream)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        if self.torch_stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.torch_stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def vector(self, t, n: int, name: str):
+        """Address of an optional contiguous [n] bf16 / fp32 vector."""
+        if t is None:
+            return None
+        if t.device != self.device or t.shape != (n,) or t.dtype not in _REAL or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 or fp32 vector of {n} on {self.device}")
+        return t.data_ptr()
+
+    def rows(self, t, M: int, C: int, dtypes, name: str) -> tuple:
+        """(address, row stride) of an optional [M, C] tensor whose rows are contiguous."""
+        if t is None:
+            return None, 0
+        if t.device != self.device or t.shape != (M, C) or t.dtype not in dtypes:
+            raise ValueError(f"{name} must be [{M}, {C}] of {dtypes} on {self.device}")
+        step, inner = t.stride()
+        if M <= 1:
+            step = C
+        if (C > 1 and inner != 1) or step < C:
+            raise ValueError(f"{name} must have contiguous rows that do not overlap")
+        return t.data_ptr(), step
+
+
+def _product_input(packed: list, X: torch.Tensor, x_scales, stream) -> tuple:
+    """Checks of a product's input: (launch, M, address of X, address of the scales)."""
+    at = _Launch(X, "X", stream)
+    if X.dim() != 2 or not X.is_contiguous():
+        raise ValueError("X must be a contiguous [M, K] tensor")
+    M, K = X.shape
+    for pk in packed:
+        if K != pk.K:
+            raise ValueError(f"X has {K} columns, the packed weight {pk.K}")
+    if x_scales is None:
+        if X.dtype != torch.bfloat16:
+            raise ValueError(f"X has dtype {X.dtype}, expected bfloat16 (or e4m3 codes with x_scales)")
+        return at, M, X.data_ptr(), None
+    if X.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise ValueError(f"X has dtype {X.dtype}, expected e4m3 codes (x_scales is given)")
+    for pk in packed:
+        if not pk.fp8:
+            raise ValueError("x_scales needs FP8 handles (patch_pack_fp8)")
+    if x_scales.device != at.device or x_scales.shape != (M,) or x_scales.dtype != torch.float32 or \
+            not x_scales.is_contiguous():
+        raise ValueError(f"x_scales must be a contiguous fp32 vector of {M} on {at.device}")
+    return at, M, X.data_ptr(), x_scales.data_ptr()
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation {name!r} is not one of {sorted(k for k in ACTIVATIONS if k)}")
+    return ACTIVATIONS[name]
+
+
+def _epilogue(at: _Launch, pk: PackedWeight, M: int, out, out_fp32: bool, bias, act: int, alpha: float,
+              residual) -> tuple:
+    """(output, PatchEpilogue) of one product, checked."""
+    want = torch.float32 if out_fp32 else torch.bfloat16
+    if out is None:
+        out, y_stride = at.empty((M, pk.N), want), pk.N
+    else:
+        _, y_stride = at.rows(out, M, pk.N, (want,), "out")
+    res, res_stride = at.rows(residual, M, pk.N, _REAL, "residual")
+    return out, PatchEpilogue(at.vector(bias, pk.N, "bias"), res, res_stride, y_stride, alpha, act,
+                              bias is not None and bias.dtype == torch.float32,
+                              residual is not None and residual.dtype == torch.float32)
+
+
+def patch_hybrid_linear(packed: PackedWeight, X: torch.Tensor, *, x_scales: torch.Tensor | None = None,
+                        bias: torch.Tensor | None = None, activation: str | None = None, alpha: float = 1.0,
+                        residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        out_fp32: bool = False, stream=None) -> torch.Tensor:
+    """residual + alpha * act(X @ W_eff^T + bias), rounded once (bf16 out, or fp32 out).
+
+    X is bf16 [M, K], or with `x_scales` (fp32 [M]) the e4m3 codes of an FP8
+    handle's input, as patch_quantize_fp8 or patch_block_norm give them.
+    activation: "relu", "gelu", "gelu_tanh", "silu" or None.  `out` may be the
+    residual itself (in place) and may have rows further apart than N."""
+    at, M, x, xs = _product_input((packed,), X, x_scales, stream)
+    out, epi = _epilogue(at, packed, M, out, out_fp32, bias, _activation(activation), alpha, residual)
+    _check("patch_hybrid_linear", load_library().patch_hybrid_linear(
+        packed.handle, x, xs, M, out.data_ptr(), 1 if out_fp32 else 0, ctypes.byref(epi), at.stream))
+    return out
+
+
+def patch_hybrid_linear_group(packed: list, X: torch.Tensor, *, x_scales: torch.Tensor | None = None,
+                              biases: list | None = None, activation: str | None = None, alpha: float = 1.0,
+                              residuals: list | None = None, outs: list | None = None, out_fp32: bool = False,
+                              stream=None) -> list:
+    """patch_hybrid_linear for 1 to 8 handles that read the same X, launched
+    together where the library can; one bias / residual / output (or None) per
+    handle, one activation and alpha for all."""
+    n = len(packed)
+    for name, given in (("biases", biases), ("residuals", residuals), ("outs", outs)):
+        if given is not None and len(given) != n:
+            raise ValueError(f"{name}: one per handle")
+    at, M, x, xs = _product_input(packed, X, x_scales, stream)
+    act = _activation(activation)
+    ys, epis = [], (PatchEpilogue * max(n, 1))()
+    for i, pk in enumerate(packed):
+        y, epis[i] = _epilogue(at, pk, M, outs[i] if outs else None, out_fp32, biases[i] if biases else None, act,
+                               alpha, residuals[i] if residuals else None)
+        ys.append(y)
+    handles = (ctypes.c_void_p * max(n, 1))(*[pk.handle for pk in packed])
+    y_p = (ctypes.c_void_p * max(n, 1))(*[y.data_ptr() for y in ys])
+    _check("patch_hybrid_linear_group", load_library().patch_hybrid_linear_group(
+        handles, n, x, xs, M, y_p, 1 if out_fp32 else 0, epis, at.stream))
+    return ys
+
+
+def patch_hybrid_gated(gate: PackedWeight, up: PackedWeight, X: torch.Tensor, *,
+                       x_scales: torch.Tensor | None = None, bias_gate: torch.Tensor | None = None,
+                       bias_up: torch.Tensor | None = None, activation: str | None = "silu",
+                       out: torch.Tensor | None = None, out_fp32: bool = False, stream=None) -> torch.Tensor:
+    """act(X @ W_gate^T + bias_gate) * (X @ W_up^T + bias_up), rounded once: the
+    gated pair of an MLP.  X, x_scales and out as patch_hybrid_linear; the two
+    biases share one dtype."""
+    if gate.N != up.N:
+        raise ValueError(f"the gate has {gate.N} rows, the up projection {up.N}")
+    if bias_gate is not None and bias_up is not None and bias_gate.dtype != bias_up.dtype:
+        raise ValueError("bias_gate and bias_up must have one dtype")
+    at, M, x, xs = _product_input((gate, up), X, x_scales, stream)
+    bg, bu = at.vector(bias_gate, gate.N, "bias_gate"), at.vector(bias_up, gate.N, "bias_up")
+    bias = bias_gate if bias_gate is not None else bias_up
+    want = torch.float32 if out_fp32 else torch.bfloat16
+    if out is None:
+        out, y_stride = at.empty((M, gate.N), want), gate.N
+    else:
+        _, y_stride = at.rows(out, M, gate.N, (want,), "out")
+    _check("patch_hybrid_gated", load_library().patch_hybrid_gated(
+        gate.handle, up.handle, x, xs, M, out.data_ptr(), y_stride, 1 if out_fp32 else 0, bg, bu,
+        1 if bias is not None and bias.dtype == torch.float32 else 0, _activation(activation), at.stream))
+    return out
+
+
+def _norm(at: _Launch, spec, C: int, name: str) -> PatchNorm:
+    """(kind, weight, bias, eps) -> PatchNorm; None is no norm."""
+    if spec is None:
+        return PatchNorm(0, 0, None, None, 0.0)
+    kind, weight, bias, eps = spec
+    if kind not in NORMS:
+        raise ValueError(f"{name} norm {kind!r} is not one of {sorted(NORMS)}")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError(f"{name}: weight and bias must have one dtype")
+    real = weight if weight is not None else bias
+    return PatchNorm(NORMS[kind], real is not None and real.dtype == torch.float32,
+                     at.vector(weight, C, f"{name} weight"), at.vector(bias, C, f"{name} bias"), eps)
+
+
+def patch_block_norm(branch: torch.Tensor, *, residual: torch.Tensor | None = None,
+                     gate: torch.Tensor | None = None, scale: float = 1.0, post: tuple | None = None,
+                     pre: tuple | None = None, z_type: str = "bf16", h_fp32: bool = False,
+                     out_h: torch.Tensor | None = None, out_z: torch.Tensor | None = None, stream=None) -> dict:
+    """The boundary between two sublayers, one pass over the rows:
+
+        h = residual + scale * gate * norm_post(branch),    z = norm_pre(h)
+
+    branch [M, C] and residual [M, C] are bf16 or fp32 with contiguous rows.
+    gate is [C], or [R, C] with R dividing M (M / R consecutive tokens share a
+    row).  post and pre are (kind, weight, bias, eps) with kind "rms" or
+    "layer" and weight, bias [C] or None; post None means no norm.  z is given
+    where there is a `pre` or z_type is "e4m3" (codes and a scale per token for
+    patch_hybrid_linear's x_scales).  out_h may be the residual or the branch,
+    out_z the branch (in place).  Returns {"h", "z", "scales"}."""
+    at = _Launch(branch, "branch", stream)
+    if branch.dim() != 2:
+        raise ValueError("branch must be [M, C]")
+    M, C = branch.shape
+    if z_type not in Z_TYPES:
+        raise ValueError(f"z_type {z_type!r} is not one of {sorted(Z_TYPES)}")
+    b, b_step = at.rows(branch, M, C, _REAL, "branch")
+    r, r_step = at.rows(residual, M, C, _REAL, "residual")
+    g, g_step, g_tokens = None, 0, 1
+    if gate is not None:
+        rows = 1 if gate.dim() == 1 else gate.shape[0]
+        if rows < 1 or M % rows:
+            raise ValueError(f"gate has {rows} rows, which do not divide {M} tokens")
+        g, g_step = at.rows(gate if gate.dim() == 2 else gate.view(1, -1), rows, C, _REAL, "gate")
+        g_tokens = max(M // rows, 1)
+    h_type = torch.float32 if h_fp32 else torch.bfloat16
+    if out_h is None:
+        out_h = at.empty((M, C), h_type)
+    h, h_step = at.rows(out_h, M, C, (h_type,), "out_h")
+    z = scales = None
+    z_step = 0
+    want = Z_TYPES[z_type] if pre is not None or z_type == "e4m3" else 0
+    if want:
+        z_dtype = (torch.bfloat16, torch.float32, torch.uint8)[want - 1]
+        if out_z is None:
+            out_z = at.empty((M, C), z_dtype)
+        z, z_step = at.rows(out_z, M, C, (z_dtype,), "out_z")
+        if want == 3:
+            scales = at.empty((M,), torch.float32)
+    elif out_z is not None:
+        raise ValueError("out_z without a pre norm")
+    args = PatchBlockNormArgs(b, b_step, r, r_step, g, g_step, g_tokens, h, h_step, z, z_step,
+                              scales.data_ptr() if scales is not None else None, _norm(at, post, C, "post"),
+                              _norm(at, pre, C, "pre"), scale, branch.dtype == torch.float32,
+                              residual is not None and residual.dtype == torch.float32,
+                              gate is not None and gate.dtype == torch.float32, h_fp32, want)
+    _check("patch_block_norm", load_library().patch_block_norm(ctypes.byref(args), M, C, at.stream))
+    return {"h": out_h, "z": out_z if want else None, "scales": scales}
 
 
 def patch_free(packed: PackedWeight, stream=None) -> None:
