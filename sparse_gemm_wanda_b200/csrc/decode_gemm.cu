@@ -55,6 +55,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "epilogue.cuh"
 #include "patch_common.cuh"
 #include "patch_internal.h"
 
@@ -134,6 +135,11 @@ struct DecodeParams {
     int stall_first_kstep;  // failure-detection test hook
     uint64_t first_desc[kDecMaxCtas];   // descriptor of chunk c for c < gridDim.x
     uint64_t second_desc[kDecMaxCtas];  // of chunk c + gridDim.x where that exists
+};
+
+// the matrices' epilogues, for the fix-up only
+struct DecodeEpi {
+    Epilogue e[kDecMaxGroup];
 };
 
 // matrix holding global band gb
@@ -563,18 +569,10 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     if (warp == 1) tmem_dealloc(tmem_base, C::kTmemCols);
 }
 
-// Fix-up: Y[m, band*128 + row] = the band's chunk partials added in chunk
-// order.  Block (band, m), one thread per row.  Launched as a programmatic
-// dependent of the GEMM; resets the chunk counter once the GEMM is complete.
+// The partials of one output added in chunk order, from zero; FP8: times both scales.
 template <int BN, bool F8>
-__global__ void __launch_bounds__(kBand)
-decode_reduce_kernel(const __grid_constant__ DecodeParams p) {
-    if (threadIdx.x == 0) pdl_trigger();  // the next GEMM may start its prologue
-    pdl_wait();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.counter = 0u;
-    const int band = blockIdx.x, m = blockIdx.y, row = threadIdx.x;
-    const int mi = dec_mat_of_band(p, band);
-    const float *src = p.partial[mi] + (static_cast<int64_t>(band - p.band0[mi]) * p.cpb * BN + m) * kBand + row;
+__device__ __forceinline__ float dec_sum(const DecodeParams &p, int mi, int band, int m, int row) {
+    const float *src = p.partial[mi] + (static_cast<int64_t>(band) * p.cpb * BN + m) * kBand + row;
     float acc = 0.0f;
     for (int c0 = 0; c0 < p.cpb; c0 += 8) {
         float v[8];
@@ -585,9 +583,44 @@ decode_reduce_kernel(const __grid_constant__ DecodeParams p) {
         for (int q = 0; q < 8; ++q)
             if (c0 + q < p.cpb) acc = __fadd_rn(acc, v[q]);
     }
-    const int64_t n = static_cast<int64_t>(band - p.band0[mi]) * kBand + row;
-    if constexpr (F8) acc = acc * __ldg(p.f8_sw[mi] + n) * __ldg(p.f8_sx + m);
-    store_out(p, mi, static_cast<int64_t>(m) * p.N[mi] + n, acc);
+    if constexpr (F8)
+        acc = acc * __ldg(p.f8_sw[mi] + static_cast<int64_t>(band) * kBand + row) * __ldg(p.f8_sx + m);
+    return acc;
+}
+
+// Fix-up: Y[m, band*128 + row] = the band's chunk partials added in chunk
+// order, then the epilogue.  Block (band, m), one thread per row; gated: the
+// bands of the first matrix, each thread adding both matrices' partials.
+// Launched as a programmatic dependent of the GEMM; resets the chunk counter
+// once the GEMM is complete.
+template <int BN, bool F8, int MODE>
+__global__ void __launch_bounds__(kBand)
+decode_reduce_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ DecodeEpi epi) {
+    if (threadIdx.x == 0) pdl_trigger();  // the next GEMM may start its prologue
+    pdl_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.counter = 0u;
+    const int m = blockIdx.y, row = threadIdx.x;
+    const int mi = dec_mat_of_band(p, blockIdx.x);
+    const int band = blockIdx.x - p.band0[mi];
+    const int64_t n = static_cast<int64_t>(band) * kBand + row;
+    if constexpr (MODE == kEpiPlain) {
+        store_out(p, mi, static_cast<int64_t>(m) * p.N[mi] + n, dec_sum<BN, F8>(p, mi, band, m, row));
+    } else {
+        const Epilogue &e = epi.e[mi];
+        float v[1];
+        const float b = epi_bias(e, n);
+        if constexpr (MODE == kEpiLinear) {
+            uint32_t r[1];
+            epi_fetch(e, p.N[mi], m, n, 1, r);
+            v[0] = dec_sum<BN, F8>(p, mi, band, m, row);
+            epi_store(e, p.Y[mi], p.y_fp32, m, n, 1, b, v, r);
+        } else {
+            const float u = dec_sum<BN, F8>(p, 1, band, m, row) + epi_bias(epi.e[1], n);
+            v[0] = dec_sum<BN, F8>(p, 0, band, m, row) + b;
+            activate(v, e.act);
+            store_real(p.Y[0], static_cast<int64_t>(m) * e.ldy + n, v[0] * u, p.y_fp32);
+        }
+    }
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -641,7 +674,7 @@ size_t decode_workspace_bytes(int nchunks, int bn) {
 namespace {
 
 template <int BN, bool F8>
-cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream) {
+cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, bool gated) {
     using C = DecCfg<BN>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
@@ -653,6 +686,7 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream) 
     if (count < 1 || count > kDecMaxGroup) return cudaErrorInvalidValue;
     const GemmLaunch &g = gs[0];
     if (F8 && !g.f8_sx) return cudaErrorInvalidValue;
+    if (gated && (count != 2 || gs[0].N != gs[1].N)) return cudaErrorInvalidValue;
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorInvalidValue;
     // X [M,K] viewed as (128-byte column blocks, M rows, K-steps): 64 bf16
@@ -674,6 +708,7 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream) 
     if (!g.counter) return cudaErrorInvalidValue;
     if (g.dec_cp < 1 || g.dec_cp > kDecChunkPairs || g.dec_cpb < 1) return cudaErrorInvalidValue;
 
+    DecodeEpi epi;
     DecodeParams p;
     p.K = g.K;
     p.M = g.M;
@@ -697,8 +732,8 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream) 
     for (int i = 0; i < count; ++i) {
         const GemmLaunch &m = gs[i];
         // one chunking, one X, one output type for the whole launch
-        if (m.K != g.K || m.M != g.M || m.X != g.X || m.y_fp32 != g.y_fp32 || m.dec_cp != g.dec_cp ||
-            m.dec_cpb != g.dec_cpb || m.N % kBand != 0 || m.dec_nchunks != (m.N / kBand) * g.dec_cpb ||
+        if (m.K != g.K || m.M != g.M || m.X != g.X || m.y_fp32 != g.y_fp32 || m.epi_on != g.epi_on ||
+            m.dec_cp != g.dec_cp || m.dec_cpb != g.dec_cpb || m.N % kBand != 0 || m.dec_nchunks != (m.N / kBand) * g.dec_cpb ||
             !m.chunk_desc || !m.chunk_desc_host || !m.packed || !m.Y || !m.status || !m.ready ||
             (F8 && (!m.f8_sw || m.f8_sx != g.f8_sx)))
             return cudaErrorInvalidValue;
@@ -707,6 +742,7 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream) 
         p.f8_sw[i] = m.f8_sw;
         p.chunk_desc[i] = m.chunk_desc;
         p.Y[i] = m.Y;
+        epi.e[i] = m.epi;
         p.N[i] = m.N;
         p.status[i] = m.status;
         p.ready[i] = m.ready;
@@ -760,10 +796,12 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream) 
     cudaError_t err = cudaLaunchKernelEx(&cfg, decode_gemm_kernel<BN, F8>, map, p);
     if (err == cudaSuccess) {
         note_launches(1);
-        cfg.gridDim = dim3(static_cast<unsigned>(bands), static_cast<unsigned>(g.M));
+        cfg.gridDim = dim3(static_cast<unsigned>(gated ? g.N / kBand : bands), static_cast<unsigned>(g.M));
         cfg.blockDim = dim3(kBand);
         cfg.dynamicSmemBytes = 0;
-        err = cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8>, p);
+        err = gated      ? cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiGated>, p, epi)
+              : g.epi_on ? cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiLinear>, p, epi)
+                         : cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiPlain>, p, epi);
         if (err == cudaSuccess) note_launches(1);
     }
     if (ws) {
@@ -775,28 +813,30 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream) 
 
 }  // namespace
 
-void preload_decode_kernels() {
+template <int BN, bool F8>
+static void preload_decode() {
     cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<16, false>);
-    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<32, false>);
-    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<64, false>);
-    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<16, false>);
-    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<32, false>);
-    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<64, false>);
-    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<16, true>);
-    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<32, true>);
-    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<64, true>);
-    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<16, true>);
-    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<32, true>);
-    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<64, true>);
+    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<BN, F8>);
+    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<BN, F8, kEpiPlain>);
+    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<BN, F8, kEpiLinear>);
+    (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<BN, F8, kEpiGated>);
 }
 
-cudaError_t launch_decode_group(const GemmLaunch *gs, int count, cudaStream_t stream) {
+void preload_decode_kernels() {
+    preload_decode<16, false>();
+    preload_decode<32, false>();
+    preload_decode<64, false>();
+    preload_decode<16, true>();
+    preload_decode<32, true>();
+    preload_decode<64, true>();
+}
+
+cudaError_t launch_decode_group(const GemmLaunch *gs, int count, cudaStream_t stream, bool gated) {
     if (count < 1) return cudaErrorInvalidValue;
     const int64_t M = gs[0].M;
-    if (M <= 16) return launch_decode<16, false>(gs, count, stream);
-    if (M <= 32) return launch_decode<32, false>(gs, count, stream);
-    if (M <= kDecodeMaxM) return launch_decode<64, false>(gs, count, stream);
+    if (M <= 16) return launch_decode<16, false>(gs, count, stream, gated);
+    if (M <= 32) return launch_decode<32, false>(gs, count, stream, gated);
+    if (M <= kDecodeMaxM) return launch_decode<64, false>(gs, count, stream, gated);
     return cudaErrorInvalidValue;
 }
 
@@ -804,12 +844,12 @@ cudaError_t launch_decode_gemm(const GemmLaunch &g, cudaStream_t stream) {
     return launch_decode_group(&g, 1, stream);
 }
 
-cudaError_t launch_decode_f8(const GemmLaunch *gs, int count, cudaStream_t stream) {
+cudaError_t launch_decode_f8(const GemmLaunch *gs, int count, cudaStream_t stream, bool gated) {
     if (count < 1) return cudaErrorInvalidValue;
     const int64_t M = gs[0].M;
-    if (M <= 16) return launch_decode<16, true>(gs, count, stream);
-    if (M <= 32) return launch_decode<32, true>(gs, count, stream);
-    if (M <= kDecodeMaxM) return launch_decode<64, true>(gs, count, stream);
+    if (M <= 16) return launch_decode<16, true>(gs, count, stream, gated);
+    if (M <= 32) return launch_decode<32, true>(gs, count, stream, gated);
+    if (M <= kDecodeMaxM) return launch_decode<64, true>(gs, count, stream, gated);
     return cudaErrorInvalidValue;
 }
 

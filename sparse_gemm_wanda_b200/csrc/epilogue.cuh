@@ -1,23 +1,46 @@
-// The epilogue of a hybrid product, computed on its fp32 sums before the one
+// The epilogue of a hybrid product, computed in fp32 on its sums before the one
 // rounding to the output type (see patch_hybrid_linear in include/patch.h).
+//
+// A product's last kernel (the GEMM, or the fix-up that joins its partials)
+// holds every sum in a register of the thread that stores it, so the epilogue
+// costs one read of the residual and no pass of its own.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "patch_common.cuh"
 #include "patch_internal.h"
 
 namespace patchk {
 
-// The activations in fp32, through CUDA's own math functions.
-__device__ __forceinline__ float activate(float v, int act) {
-    switch (act) {
-        case kActRelu: return v < 0.0f ? 0.0f : v;  // NaN stays NaN
-        case kActGelu: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-        case kActGeluTanh: return 0.5f * v * (1.0f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
-        case kActSilu: return v / (1.0f + expf(-v));
-        default: return v;
+// What the last kernel of a product does with its sums.
+enum EpiMode { kEpiPlain = 0, kEpiLinear = 1, kEpiGated = 2 };
+
+// The activations, through CUDA's own math functions.
+__device__ __forceinline__ float act_relu(float v) { return v < 0.0f ? 0.0f : v; }  // NaN stays NaN
+__device__ __forceinline__ float act_gelu(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678f)); }
+__device__ __forceinline__ float act_gelu_tanh(float v) {
+    return 0.5f * v * (1.0f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
+}
+__device__ __forceinline__ float act_silu(float v) { return v / (1.0f + expf(-v)); }
+
+// `act` is the same for the whole launch: one uniform branch per NV values.
+template <int NV>
+__device__ __forceinline__ void activate(float (&v)[NV], int act) {
+    if (act == kActSilu) {
+#pragma unroll
+        for (int q = 0; q < NV; ++q) v[q] = act_silu(v[q]);
+    } else if (act == kActGelu) {
+#pragma unroll
+        for (int q = 0; q < NV; ++q) v[q] = act_gelu(v[q]);
+    } else if (act == kActGeluTanh) {
+#pragma unroll
+        for (int q = 0; q < NV; ++q) v[q] = act_gelu_tanh(v[q]);
+    } else if (act == kActRelu) {
+#pragma unroll
+        for (int q = 0; q < NV; ++q) v[q] = act_relu(v[q]);
     }
 }
 
@@ -30,6 +53,116 @@ __device__ __forceinline__ void store_real(void *p, int64_t i, float v, int fp32
         static_cast<float *>(p)[i] = v;
     else
         static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float epi_bias(const Epilogue &e, int64_t n) {
+    return e.bias ? load_real(e.bias, n, e.bias_fp32) : 0.0f;
+}
+
+// NV values to consecutive rows of a column, `ld` elements apart.
+template <int NV>
+__device__ __forceinline__ void store_column(void *Y, int64_t i, int64_t ld, int count, const float (&v)[NV],
+                                             int fp32) {
+    if (fp32) {
+        float *y = static_cast<float *>(Y) + i;
+#pragma unroll
+        for (int q = 0; q < NV; ++q)
+            if (q < count) y[q * ld] = v[q];
+    } else {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(Y) + i;
+#pragma unroll
+        for (int q = 0; q < NV; ++q)
+            if (q < count) y[q * ld] = __float2bfloat16_rn(v[q]);
+    }
+}
+
+// NV consecutive tokens m0 .. m0 + count - 1 (count <= NV) of output column n.
+// epi_fetch reads what the epilogue adds (or multiplies by), as stored, and is
+// called before the sums are ready; epi_store finishes and stores them.  The
+// values are converted only there: a conversion right behind its load would
+// make every load wait for the one before it.
+template <int NV>
+__device__ __forceinline__ void epi_fetch(const Epilogue &e, int64_t N, int64_t m0, int64_t n, int count,
+                                          uint32_t (&r)[NV]) {
+#pragma unroll
+    for (int q = 0; q < NV; ++q) r[q] = 0u;
+    if (e.mul) {
+        const float *src = e.mul + m0 * N + n;
+#pragma unroll
+        for (int q = 0; q < NV; ++q)
+            if (q < count) r[q] = __float_as_uint(src[q * N]);
+    } else if (e.residual && e.res_fp32) {
+        const float *src = static_cast<const float *>(e.residual) + m0 * e.ldr + n;
+#pragma unroll
+        for (int q = 0; q < NV; ++q)
+            if (q < count) r[q] = __float_as_uint(src[q * e.ldr]);
+    } else if (e.residual) {
+        const uint16_t *src = static_cast<const uint16_t *>(e.residual) + m0 * e.ldr + n;
+#pragma unroll
+        for (int q = 0; q < NV; ++q)
+            if (q < count) r[q] = src[q * e.ldr];
+    }
+}
+
+template <int NV>
+__device__ __forceinline__ void epi_store(const Epilogue &e, void *Y, int y_fp32, int64_t m0, int64_t n, int count,
+                                          float bias, float (&v)[NV], const uint32_t (&r)[NV]) {
+#pragma unroll
+    for (int q = 0; q < NV; ++q) v[q] += bias;
+    activate(v, e.act);
+    const int shift = e.mul || e.res_fp32 ? 0 : 16;
+#pragma unroll
+    for (int q = 0; q < NV; ++q) {
+        const float a = __uint_as_float(r[q] << shift);
+        v[q] = e.mul ? v[q] * a : fmaf(e.alpha, v[q], a);
+    }
+    store_column(Y, m0 * e.ldy + n, e.ldy, count, v, y_fp32);
+}
+
+// One piece of a gated item in a two-SM kernel: this thread's output column n
+// (TMEM lane) for the 16-token chunks 16 * grp + 32 j of an accumulator at
+// tensor-memory address `acc`; `sums(c0, v)` reads a chunk's sums.
+//   gate (mi = 0): act(sum + bias), written back in place chunk by chunk (one
+//     copy of the activation code), then held in 128 registers so that the
+//     accumulator is free for the next item while the up projection runs;
+//   up (mi = 1): (sum + bias) * the held gate, stored.
+template <class Sums>
+__device__ __forceinline__ void gated_piece(const Epilogue &e, void *Y, int y_fp32, int mi, uint32_t acc, int grp,
+                                            int64_t m_base, int m_valid, int64_t n, float bias,
+                                            uint32_t (&held)[8][16], const Sums &sums) {
+    if (mi == 0) {
+#pragma unroll 1
+        for (int c0 = 16 * grp; c0 < m_valid; c0 += 32) {
+            float v[16];
+            uint32_t r[16];
+            sums(c0, v);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] += bias;
+            activate(v, e.act);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) r[q] = __float_as_uint(v[q]);
+            tmem_st_32x32b_x16(acc + static_cast<uint32_t>(c0), r);
+        }
+        tmem_st_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (16 * grp + 32 * j < m_valid)
+                tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(16 * grp + 32 * j), held[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tmem_ld_wait(held[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c0 = 16 * grp + 32 * j;
+            if (c0 < m_valid) {
+                float v[16];
+                sums(c0, v);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) v[q] = (v[q] + bias) * __uint_as_float(held[j][q]);
+                store_column(Y, (m_base + c0) * e.ldy + n, e.ldy, m_valid - c0, v, y_fp32);
+            }
+        }
+    }
 }
 
 }  // namespace patchk

@@ -34,6 +34,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "epilogue.cuh"
 #include "patch_common.cuh"
 #include "patch_internal.h"
 
@@ -62,6 +63,7 @@ struct F8Params {
     void *Y;
     int y_fp32;
     uint32_t *status;
+    Epilogue epi;
 };
 
 // Work item w: tile w / ksplit, k-steps [c0, c1) of it.
@@ -92,7 +94,7 @@ struct F8Cfg {
     static_assert(kCols <= 512, "tensor memory holds 512 columns");
 };
 
-template <int BN>
+template <int BN, bool EPI>
 __global__ void __launch_bounds__(kF8Threads, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ F8Params p) {
     using C = F8Cfg<BN>;
@@ -299,9 +301,24 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                         if (c0 + q < m_valid) part[(c0 + q) * kBand] = __uint_as_float(r[q]);
                 }
             } else if (*abort_flag == 0) {
+                [[maybe_unused]] float bias = 0.0f;
+                if constexpr (EPI) bias = epi_bias(p.epi, n);
 #pragma unroll 1
                 for (int c0 = 0; c0 < m_valid; c0 += 16) {
                     uint32_t r[16];
+                    if constexpr (EPI) {
+                        uint32_t add[16];
+                        float v[16];
+                        epi_fetch(p.epi, p.N, m_base + c0, n, m_valid - c0, add);
+                        tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
+                        tmem_ld_wait(r);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            v[q] = c0 + q < m_valid
+                                       ? __uint_as_float(r[q]) * swn * __ldg(p.sx + m_base + c0 + q) : 0.0f;
+                        epi_store(p.epi, p.Y, p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
+                        continue;
+                    }
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
                     tmem_ld_wait();
 #pragma unroll
@@ -327,7 +344,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
 // order, from zero) * sw[n] * sx[m].  Block (tile, token of the tile), one
 // thread per row of the band.  Launched as a programmatic dependent of the
 // GEMM; waits for it.
-template <int BN>
+template <int BN, bool EPI>
 __global__ void __launch_bounds__(kBand)
 fp8_splitk_reduce_kernel(const __grid_constant__ F8Params p) {
     if (threadIdx.x == 0) pdl_trigger();
@@ -337,6 +354,13 @@ fp8_splitk_reduce_kernel(const __grid_constant__ F8Params p) {
     const int64_t m = static_cast<int64_t>(tt) * BN + ml;
     if (m >= p.M) return;
     const float *src = p.partial + (static_cast<int64_t>(tile) * p.ksplit * BN + ml) * kBand + row;
+    const int64_t n = static_cast<int64_t>(band) * kBand + row;
+    [[maybe_unused]] uint32_t add[1];
+    [[maybe_unused]] float bias = 0.0f;
+    if constexpr (EPI) {
+        epi_fetch(p.epi, p.N, m, n, 1, add);
+        bias = epi_bias(p.epi, n);
+    }
     float acc = 0.0f;
     for (int k0 = 0; k0 < p.ksplit; k0 += 8) {
         float v[8];
@@ -347,8 +371,13 @@ fp8_splitk_reduce_kernel(const __grid_constant__ F8Params p) {
         for (int q = 0; q < 8; ++q)
             if (k0 + q < p.ksplit) acc = __fadd_rn(acc, v[q]);
     }
-    const int64_t n = static_cast<int64_t>(band) * kBand + row;
-    store_y(p, m * p.N + n, acc * __ldg(p.sw + n) * __ldg(p.sx + m));
+    acc = acc * __ldg(p.sw + n) * __ldg(p.sx + m);
+    if constexpr (EPI) {
+        float v[1] = {acc};
+        epi_store(p.epi, p.Y, p.y_fp32, m, n, 1, bias, v, add);
+    } else {
+        store_y(p, m * p.N + n, acc);
+    }
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -370,13 +399,13 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-template <int BN>
-cudaError_t run_fp8(const Fp8Launch &g, cudaStream_t stream) {
+template <int BN, bool EPI>
+cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     using C = F8Cfg<BN>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr_err = cudaFuncSetAttribute(fp8_gemm_kernel<BN, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         C::kSmem);
     });
     if (attr_err != cudaSuccess) return attr_err;
@@ -408,6 +437,7 @@ cudaError_t run_fp8(const Fp8Launch &g, cudaStream_t stream) {
     p.Y = g.Y;
     p.y_fp32 = g.y_fp32;
     p.status = g.status;
+    p.epi = g.epi;
     // at most half as many tiles as SMs: split each tile's k-steps so that
     // about two work items fall on every SM (ranges of equal length, none
     // empty); with more tiles the partials and the fix-up cost more than the
@@ -442,7 +472,7 @@ cudaError_t run_fp8(const Fp8Launch &g, cudaStream_t stream) {
     kcfg.stream = stream;
     kcfg.attrs = attr;
     kcfg.numAttrs = 1;
-    cudaError_t err = cudaLaunchKernelEx(&kcfg, fp8_gemm_kernel<BN>, map, p);
+    cudaError_t err = cudaLaunchKernelEx(&kcfg, fp8_gemm_kernel<BN, EPI>, map, p);
     if (err == cudaSuccess) note_launches(1);
     if (err == cudaSuccess && p.ksplit > 1) {
         cudaLaunchConfig_t cfg = {};
@@ -452,7 +482,7 @@ cudaError_t run_fp8(const Fp8Launch &g, cudaStream_t stream) {
         cfg.stream = stream;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        err = cudaLaunchKernelEx(&cfg, fp8_splitk_reduce_kernel<BN>, p);
+        err = cudaLaunchKernelEx(&cfg, fp8_splitk_reduce_kernel<BN, EPI>, p);
         if (err == cudaSuccess) note_launches(1);
     }
     if (ws) {
@@ -462,24 +492,39 @@ cudaError_t run_fp8(const Fp8Launch &g, cudaStream_t stream) {
     return err;
 }
 
+template <int BN>
+cudaError_t run_fp8(const Fp8Launch &g, cudaStream_t stream) {
+    return g.epi_on ? run_fp8_mode<BN, true>(g, stream) : run_fp8_mode<BN, false>(g, stream);
+}
+
+template <int BN, bool EPI>
+void preload_fp8() {
+    cudaFuncAttributes a;
+    (void)cudaFuncGetAttributes(&a, fp8_gemm_kernel<BN, EPI>);
+    (void)cudaFuncGetAttributes(&a, fp8_splitk_reduce_kernel<BN, EPI>);
+}
+
 }  // namespace
 
 void preload_fp8_gemm_kernels() {
-    cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, fp8_gemm_kernel<64>);
-    (void)cudaFuncGetAttributes(&a, fp8_gemm_kernel<128>);
-    (void)cudaFuncGetAttributes(&a, fp8_gemm_kernel<240>);
-    (void)cudaFuncGetAttributes(&a, fp8_splitk_reduce_kernel<64>);
-    (void)cudaFuncGetAttributes(&a, fp8_splitk_reduce_kernel<128>);
-    (void)cudaFuncGetAttributes(&a, fp8_splitk_reduce_kernel<240>);
+    preload_fp8<64, false>();
+    preload_fp8<128, false>();
+    preload_fp8<240, false>();
+    preload_fp8<64, true>();
+    preload_fp8<128, true>();
+    preload_fp8<240, true>();
+}
+
+bool takes_duo_fp8(const Fp8Launch &g) {
+    // more than one token tile: the two-SM kernel, where the bands pair up
+    // (prefill table) and the k-step count is even
+    const bool duo_ok = g.ptable && (g.N / kBand) % 2 == 0 && (g.K / kF8Step) % 2 == 0 && g.K / kF8Step <= 224;
+    return duo_ok && g.force_kernel != 1 && (g.M > 128 || g.force_kernel == 3);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream) {
     if (g.K % kF8Step != 0 || g.N % kBand != 0 || g.M < 1) return cudaErrorInvalidValue;
-    // more than one token tile: the two-SM kernel, where the bands pair up
-    // (prefill table) and the k-step count is even
-    const bool duo_ok = g.ptable && (g.N / kBand) % 2 == 0 && (g.K / kF8Step) % 2 == 0 && g.K / kF8Step <= 224;
-    if (duo_ok && g.force_kernel != 1 && (g.M > 128 || g.force_kernel == 3)) {
+    if (takes_duo_fp8(g)) {
         const DuoFp8Plan dp = plan_duo_fp8(g.N, g.M, g.num_sms, g.all_sparse != 0);
         if (dp.bn > 0) return launch_duo_fp8(g, dp, stream);
     }

@@ -60,6 +60,7 @@
 #include <mutex>
 #include <vector>
 
+#include "epilogue.cuh"
 #include "patch_common.cuh"
 #include "patch_internal.h"
 
@@ -114,6 +115,7 @@ struct GemmParams {
     const uint32_t *ready;  // set (release) by the packer once the packed bytes are final
     int stall_first_kstep;  // failure-detection test hook: CTA 0 never loads its first k-step
     int32_t u0[kMaxStreamKCtas + 1];  // stream-K: first unit of every CTA (u0[P] = units)
+    Epilogue epi;
 };
 
 // One piece of work of a CTA: k-steps [ks0, ks1) of tile (band, ttile).
@@ -220,7 +222,7 @@ __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-template <int BN, int STAGES, bool NM>
+template <int BN, int STAGES, bool NM, bool EPI>
 __global__ void __launch_bounds__(NM ? kGemmThreadsNM : kGemmThreads, 1)
 hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ GemmParams p) {
     using C = GemmCfg<BN, STAGES>;
@@ -541,9 +543,15 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             const int m_valid = static_cast<int>(min(static_cast<int64_t>(BN), p.M - m_base));
             float *part = (sg.nsegs > 1) ? p.partial + static_cast<int64_t>(sg.slot) * BN * kBand
                                          : nullptr;
+            [[maybe_unused]] float bias = 0.0f;
+            if constexpr (EPI) bias = epi_bias(p.epi, n);
 #pragma unroll 1
             for (int c0 = 0; c0 < BN; c0 += 16) {
                 uint32_t r[16];
+                [[maybe_unused]] uint32_t add[16];
+                if constexpr (EPI) {
+                    if (!part && live) epi_fetch(p.epi, p.N, m_base + c0, n, m_valid - c0, add);
+                }
                 tmem_ld_32x32b_x16(lane_base + buf * BN + c0, r);
                 tmem_ld_wait();
                 if (!live) continue;
@@ -551,6 +559,11 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         if (c0 + q < m_valid) part[(c0 + q) * kBand + row] = __uint_as_float(r[q]);
+                } else if constexpr (EPI) {
+                    float v[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
+                    epi_store(p.epi, p.Y, p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
                 } else {
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
@@ -573,7 +586,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 // Stream-K fix-up: for every tile shared by several CTAs, Y = the partials of
 // its CTAs added in CTA order (fixed order: the result does not depend on
 // timing).  Launched as a programmatic dependent of the GEMM; waits for it.
-template <int BN>
+template <int BN, bool EPI>
 __global__ void __launch_bounds__(256)
 streamk_reduce_kernel(const float *__restrict__ partial, const __grid_constant__ GemmParams p,
                       int P) {
@@ -606,6 +619,13 @@ streamk_reduce_kernel(const float *__restrict__ partial, const __grid_constant__
     if (e >= m_valid * kBand) return;
     const int m = e / kBand, row = e % kBand;
     const float *src = partial + m * kBand + row;
+    const int64_t n = static_cast<int64_t>(band) * kBand + row;
+    [[maybe_unused]] uint32_t add[1];
+    [[maybe_unused]] float bias = 0.0f;
+    if constexpr (EPI) {
+        epi_fetch(p.epi, N, m_base + m, n, 1, add);
+        bias = epi_bias(p.epi, n);
+    }
     float acc = 0.0f;
     for (int j0 = 0; j0 < ns; j0 += 8) {
         float v[8];
@@ -616,11 +636,12 @@ streamk_reduce_kernel(const float *__restrict__ partial, const __grid_constant__
         for (int q = 0; q < 8; ++q)
             if (j0 + q < ns) acc = __fadd_rn(acc, v[q]);
     }
-    const int64_t yi = (m_base + m) * N + static_cast<int64_t>(band) * kBand + row;
-    if (y_fp32)
-        static_cast<float *>(Y)[yi] = acc;
-    else
-        static_cast<__nv_bfloat16 *>(Y)[yi] = __float2bfloat16_rn(acc);
+    if constexpr (EPI) {
+        float v[1] = {acc};
+        epi_store(p.epi, Y, y_fp32, m_base + m, n, 1, bias, v, add);
+    } else {
+        store_real(Y, (m_base + m) * N + n, acc, y_fp32);
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -702,15 +723,15 @@ void streamk_bounds(const GemmLaunch &g, GemmParams &p, int bn, int P) {
         if (p.u0[c] >= p.u0[c + 1]) p.u0[c] = p.u0[c + 1] - 1;
 }
 
-template <int BN, int STAGES, bool NM = false>
-cudaError_t run(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
+template <int BN, int STAGES, bool NM, bool EPI>
+cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
     using C = GemmCfg<BN, STAGES>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     constexpr int kSmem = C::kSmemBytes + (NM ? kLutBytes : 0);
     static_assert(kSmem <= 232448, "shared memory per CTA");
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(hybrid_gemm_kernel<BN, STAGES, NM>,
+        attr_err = cudaFuncSetAttribute(hybrid_gemm_kernel<BN, STAGES, NM, EPI>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (attr_err != cudaSuccess) return attr_err;
@@ -730,6 +751,7 @@ cudaError_t run(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
     p.status = g.status;
     p.ready = g.ready;
     p.stall_first_kstep = g.stall_first_kstep;
+    p.epi = g.epi;
     const int64_t tiles = static_cast<int64_t>(p.bands) * p.ttiles;
     const int64_t slots = static_cast<int64_t>(g.num_sms) * ctas_per_sm;
     // whole tiles when there are at least two waves of them, stream-K otherwise
@@ -766,13 +788,13 @@ cudaError_t run(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, hybrid_gemm_kernel<BN, STAGES, NM>, map, p);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, hybrid_gemm_kernel<BN, STAGES, NM, EPI>, map, p);
     if (err == cudaSuccess) note_launches(1);
     if (err == cudaSuccess && sk) {
         cfg.gridDim = dim3(static_cast<unsigned>((BN * kBand + 255) / 256), static_cast<unsigned>(tiles));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
-        err = cudaLaunchKernelEx(&cfg, streamk_reduce_kernel<BN>, static_cast<const float *>(ws), p,
+        err = cudaLaunchKernelEx(&cfg, streamk_reduce_kernel<BN, EPI>, static_cast<const float *>(ws), p,
                                  static_cast<int>(grid));
         if (err == cudaSuccess) note_launches(1);
     }
@@ -783,18 +805,30 @@ cudaError_t run(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
     return err;
 }
 
+template <int BN, int STAGES, bool NM = false>
+cudaError_t run(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
+    return g.epi_on ? run_mode<BN, STAGES, NM, true>(g, ctas_per_sm, stream)
+                    : run_mode<BN, STAGES, NM, false>(g, ctas_per_sm, stream);
+}
+
+template <bool EPI>
+void preload_modes() {
+    cudaFuncAttributes a;
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, false, EPI>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, false, EPI>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<160, 3, false, EPI>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, true, EPI>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, true, EPI>);
+    (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<64, EPI>);
+    (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<128, EPI>);
+    (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<160, EPI>);
+}
+
 }  // namespace
 
 void preload_hybrid_kernels() {
-    cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, false>);
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, false>);
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<160, 3, false>);
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, true>);
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, true>);
-    (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<64>);
-    (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<128>);
-    (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<160>);
+    preload_modes<false>();
+    preload_modes<true>();
 }
 
 cudaError_t launch_hybrid_gemm(const GemmLaunch &g, cudaStream_t stream) {
@@ -812,7 +846,7 @@ cudaError_t launch_hybrid_gemm(const GemmLaunch &g, cudaStream_t stream) {
         const DuoPlan dp = plan_duo_gemm(g.N, g.M, g.num_sms, g.max_pair_bytes);
         if (dp.bn > 0) return launch_duo_gemm(g, dp, stream);
     }
-    if (g.force_kernel == 4 && g.duo_ok && g.K / kStep <= 448) {
+    if (g.force_kernel == 4 && !g.epi_on && g.duo_ok && g.K / kStep <= 448) {
         const QuadPlan qp = plan_quad_gemm(g.N, g.M, g.num_sms);
         if (qp.bn > 0) return launch_quad_gemm(g, qp, stream);
     }
@@ -889,6 +923,19 @@ bool plan_hybrid_group(const GemmLaunch *gs, int count, DuoPlan *plan) {
     const DuoPlan dp = plan_duo_gemm(sum_n, g.M, g.num_sms, max_pair);
     if (dp.bn == 0) return false;
     if (g.force_kernel == 0 && dp.cost > own) return false;
+    *plan = dp;
+    return true;
+}
+
+bool plan_hybrid_gated(const GemmLaunch *gs, DuoPlan *plan) {
+    const GemmLaunch &g = gs[0];
+    if (g.M <= 128 && g.force_kernel != 3) return false;
+    if (g.force_kernel != 0 && g.force_kernel != 3) return false;
+    if (!gs[0].duo_ok || !gs[1].duo_ok || g.K / kStep > 448) return false;
+    // an item is both matrices' band pair: twice the k-steps of one product
+    const DuoPlan dp = plan_duo_gemm(g.N, g.M, g.num_sms, std::max(gs[0].max_pair_bytes, gs[1].max_pair_bytes));
+    if (dp.bn == 0) return false;
+    if (g.force_kernel == 0 && 2 * dp.cost > own_prefill_cost(gs[0]) + own_prefill_cost(gs[1])) return false;
     *plan = dp;
     return true;
 }

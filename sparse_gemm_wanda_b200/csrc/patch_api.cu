@@ -161,6 +161,13 @@ patch_status from_cuda(cudaError_t e) {
     return PATCH_ERR_CUDA;
 }
 
+// epi null: the plain product
+template <class Launch>
+void set_epilogue(Launch &g, const patchk::Epilogue *epi) {
+    g.epi_on = epi ? 1 : 0;
+    if (epi) g.epi = *epi;
+}
+
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace
@@ -423,7 +430,6 @@ static void preload_gemm_kernels() {
     patchk::preload_duo_fp8_kernels();
     patchk::preload_fp8_quantize_kernels();
     patchk::preload_pack_kernels();
-    patchk::preload_epilogue_kernels();
     if (named) done.insert(id);
 }
 
@@ -883,8 +889,9 @@ patch_status patch_packed_fp8_scales(const patch_packed *Wp, float *scales_dst, 
 // The split-K launch description of one FP8 handle's product on X codes xq
 // with token scales sx.
 static patchk::GemmLaunch fp8_split_launch(const patch_packed *Wp, const uint8_t *xq, const float *sx, int64_t M,
-                                           void *Y, int32_t y_is_fp32) {
+                                           void *Y, int32_t y_is_fp32, const patchk::Epilogue *epi) {
     patchk::GemmLaunch g = {};
+    set_epilogue(g, epi);
     g.packed = Wp->packed;
     g.table = Wp->table;
     g.N = Wp->shp.N;
@@ -913,8 +920,9 @@ static patchk::GemmLaunch fp8_split_launch(const patch_packed *Wp, const uint8_t
 
 // the launch description of one FP8 handle's product on quantised X
 static patchk::Fp8Launch fp8_launch(const patch_packed *Wp, const uint8_t *xq, const float *sx, int64_t M,
-                                    void *Y, int32_t y_is_fp32) {
+                                    void *Y, int32_t y_is_fp32, const patchk::Epilogue *epi) {
     patchk::Fp8Launch g;
+    set_epilogue(g, epi);
     g.packed = Wp->packed;
     g.table = Wp->table;
     g.ptable = Wp->ptable;
@@ -935,42 +943,63 @@ static patchk::Fp8Launch fp8_launch(const patch_packed *Wp, const uint8_t *xq, c
     return g;
 }
 
-// x_scales non-null: X holds e4m3 codes already and nothing is quantised.
-static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
-                             int32_t y_is_fp32, cudaStream_t stream) {
+// The e4m3 codes and token scales an FP8 product reads: the caller's own
+// (x_scales given), or X quantised into the handle's scratch (decode token
+// counts) or a pool block for the call (`block`, freed by free_codes).
+struct XCodes {
+    const uint8_t *q = nullptr;
+    const float *s = nullptr;
+    uint8_t *block = nullptr;
+};
+
+static cudaError_t codes_of(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, XCodes *out,
+                            cudaStream_t stream) {
+    if (x_scales) {
+        out->q = static_cast<const uint8_t *>(X);
+        out->s = x_scales;
+        return cudaSuccess;
+    }
     const int64_t K = Wp->shp.K;
-    const int force = g_test_kernel.load(std::memory_order_relaxed);
-    // decode token counts: the split-K kernel on the e4m3 codes, the weights
-    // read once over every SM; the fix-up applies the row and token scales
-    const bool split = M <= patchk::kDecodeMaxM && Wp->dec_nchunks > 0 && force == 0;
-    auto product = [&](const uint8_t *xq, const float *sx) {
-        if (!split) return patchk::launch_fp8_gemm(fp8_launch(Wp, xq, sx, M, Y, y_is_fp32), stream);
-        const patchk::GemmLaunch g = fp8_split_launch(Wp, xq, sx, M, Y, y_is_fp32);
-        return patchk::launch_decode_f8(&g, 1, stream);
-    };
-    if (x_scales) return from_cuda(product(static_cast<const uint8_t *>(X), x_scales));
-    // the activations' codes and token scales
     const size_t off_sx = round_up(static_cast<size_t>(M * K), 256);
-    const size_t bytes = off_sx + sizeof(float) * static_cast<size_t>(M);
-    uint8_t *ws = nullptr;
-    const bool own = M <= kFp8ScratchRows && Wp->fp8_xscratch;
-    cudaError_t e = cudaSuccess;
-    if (own)
-        ws = Wp->fp8_xscratch;
-    else
-        e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes, Wp->pool, stream);
-    if (e != cudaSuccess) return from_cuda(e);
+    uint8_t *ws = M <= kFp8ScratchRows ? Wp->fp8_xscratch : nullptr;
+    if (!ws) {
+        const cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws),
+                                                      off_sx + sizeof(float) * static_cast<size_t>(M), Wp->pool, stream);
+        if (e != cudaSuccess) return e;
+        out->block = ws;
+    }
     float *sx = reinterpret_cast<float *>(ws + off_sx);
-    e = patchk::launch_fp8_quantize_rows(X, M, K, ws, sx, stream);
-    if (e == cudaSuccess) e = product(ws, sx);
-    const cudaError_t e2 = own ? cudaSuccess : cudaFreeAsync(ws, stream);
+    out->q = ws;
+    out->s = sx;
+    return patchk::launch_fp8_quantize_rows(X, M, K, ws, sx, stream);
+}
+
+static patch_status free_codes(const XCodes &x, cudaError_t e, cudaStream_t stream) {
+    const cudaError_t e2 = x.block ? cudaFreeAsync(x.block, stream) : cudaSuccess;
     return from_cuda(e != cudaSuccess ? e : e2);
+}
+
+static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
+                             int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream) {
+    XCodes x;
+    cudaError_t e = codes_of(Wp, X, x_scales, M, &x, stream);
+    const int force = g_test_kernel.load(std::memory_order_relaxed);
+    if (e == cudaSuccess && M <= patchk::kDecodeMaxM && Wp->dec_nchunks > 0 && force == 0) {
+        // decode token counts: the split-K kernel on the e4m3 codes, the weights
+        // read once over every SM; the fix-up applies the row and token scales
+        const patchk::GemmLaunch g = fp8_split_launch(Wp, x.q, x.s, M, Y, y_is_fp32, epi);
+        e = patchk::launch_decode_f8(&g, 1, stream);
+    } else if (e == cudaSuccess) {
+        e = patchk::launch_fp8_gemm(fp8_launch(Wp, x.q, x.s, M, Y, y_is_fp32, epi), stream);
+    }
+    return free_codes(x, e, stream);
 }
 
 // the launch description of one bf16 handle's product
 static patchk::GemmLaunch gemm_launch(const patch_packed *Wp, const void *X_bf16, int64_t M, void *Y,
-                                      int32_t y_is_fp32) {
+                                      int32_t y_is_fp32, const patchk::Epilogue *epi) {
     patchk::GemmLaunch g;
+    set_epilogue(g, epi);
     g.packed = Wp->packed;
     g.table = Wp->table;
     g.N = Wp->shp.N;
@@ -1005,10 +1034,9 @@ static patchk::GemmLaunch gemm_launch(const patch_packed *Wp, const void *X_bf16
 }
 
 static patch_status product_one(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
-                                int32_t y_is_fp32, cudaStream_t stream) {
-    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, stream);
-    const patchk::GemmLaunch g = gemm_launch(Wp, X, M, Y, y_is_fp32);
-    return from_cuda(patchk::launch_hybrid_gemm(g, stream));
+                                int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream) {
+    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, epi, stream);
+    return from_cuda(patchk::launch_hybrid_gemm(gemm_launch(Wp, X, M, Y, y_is_fp32, epi), stream));
 }
 
 patch_status patch_hybrid_gemm(const patch_packed *Wp, const void *X_bf16, int64_t M, void *Y,
@@ -1019,13 +1047,15 @@ patch_status patch_hybrid_gemm(const patch_packed *Wp, const void *X_bf16, int64
     if (!aligned16(X_bf16) || !aligned16(Y)) return PATCH_ERR_INVALID_ARG;
     if (y_is_fp32 != 0 && y_is_fp32 != 1) return PATCH_ERR_INVALID_ARG;
     if (M > (int64_t(1) << 31)) return PATCH_ERR_INVALID_ARG;
-    return product_one(Wp, X_bf16, nullptr, M, Y, y_is_fp32, static_cast<cudaStream_t>(stream_v));
+    return product_one(Wp, X_bf16, nullptr, M, Y, y_is_fp32, nullptr, static_cast<cudaStream_t>(stream_v));
 }
 
 // The products of handles that read the same X (checked by the caller), in
 // one launch where the library can (see patch_hybrid_gemm_group).
 static patch_status products(const patch_packed *const *Wps, int32_t count, const void *X, const float *x_scales,
-                             int64_t M, void *const *Ys, int32_t y_is_fp32, cudaStream_t stream) {
+                             int64_t M, void *const *Ys, int32_t y_is_fp32, const patchk::Epilogue *epis,
+                             cudaStream_t stream) {
+    auto epi = [epis](int i) { return epis ? epis + i : nullptr; };
     const int64_t K = Wps[0]->shp.K;
     const int force = g_test_kernel.load(std::memory_order_relaxed);
     // FP8 handles: X is quantised once (into the first handle's scratch) and
@@ -1035,19 +1065,12 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
         f8_group = Wps[i]->pattern == 8 && Wps[i]->shp.K == K && Wps[i]->dec_nchunks > 0 &&
                    Wps[i]->num_sms == Wps[0]->num_sms && Wps[0]->fp8_xscratch;
     if (f8_group) {
-        const uint8_t *xq = static_cast<const uint8_t *>(X);
-        const float *sx = x_scales;
-        if (!x_scales) {
-            uint8_t *q = Wps[0]->fp8_xscratch;
-            float *s = reinterpret_cast<float *>(q + round_up(static_cast<size_t>(M * K), 256));
-            const cudaError_t e = patchk::launch_fp8_quantize_rows(X, M, K, q, s, stream);
-            if (e != cudaSuccess) return from_cuda(e);
-            xq = q;
-            sx = s;
-        }
+        XCodes x;
+        const cudaError_t e = codes_of(Wps[0], X, x_scales, M, &x, stream);
+        if (e != cudaSuccess) return free_codes(x, e, stream);
         patchk::GemmLaunch gs[patchk::kDecMaxGroup];
-        for (int i = 0; i < count; ++i) gs[i] = fp8_split_launch(Wps[i], xq, sx, M, Ys[i], y_is_fp32);
-        return from_cuda(patchk::launch_decode_f8(gs, count, stream));
+        for (int i = 0; i < count; ++i) gs[i] = fp8_split_launch(Wps[i], x.q, x.s, M, Ys[i], y_is_fp32, epi(i));
+        return free_codes(x, patchk::launch_decode_f8(gs, count, stream), stream);
     }
     if (count > 1 && M > 128 && (force == 0 || force == 3)) {
         // FP8 prefill: X quantised once, then one two-SM launch over every
@@ -1072,23 +1095,14 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
         patchk::DuoFp8Plan dp{};
         if (ok) dp = patchk::plan_duo_fp8(sum_n, M, Wps[0]->num_sms, all_sparse);
         if (ok && dp.bn > 0 && (force == 3 || dp.cost <= own)) {
-            auto launch = [&](const uint8_t *xq, const float *sx) {
+            XCodes x;
+            cudaError_t e = codes_of(Wps[0], X, x_scales, M, &x, stream);
+            if (e == cudaSuccess) {
                 patchk::Fp8Launch gs[patchk::kDecMaxGroup];
-                for (int i = 0; i < count; ++i) gs[i] = fp8_launch(Wps[i], xq, sx, M, Ys[i], y_is_fp32);
-                return patchk::launch_duo_fp8_group(gs, count, dp, stream);
-            };
-            if (x_scales) return from_cuda(launch(static_cast<const uint8_t *>(X), x_scales));
-            const size_t off_sx = round_up(static_cast<size_t>(M * K), 256);
-            uint8_t *ws = nullptr;
-            cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws),
-                                                    off_sx + sizeof(float) * static_cast<size_t>(M),
-                                                    Wps[0]->pool, stream);
-            if (e != cudaSuccess) return from_cuda(e);
-            float *sx = reinterpret_cast<float *>(ws + off_sx);
-            e = patchk::launch_fp8_quantize_rows(X, M, K, ws, sx, stream);
-            if (e == cudaSuccess) e = launch(ws, sx);
-            const cudaError_t e2 = cudaFreeAsync(ws, stream);
-            return from_cuda(e != cudaSuccess ? e : e2);
+                for (int i = 0; i < count; ++i) gs[i] = fp8_launch(Wps[i], x.q, x.s, M, Ys[i], y_is_fp32, epi(i));
+                e = patchk::launch_duo_fp8_group(gs, count, dp, stream);
+            }
+            return free_codes(x, e, stream);
         }
     }
     if (count > 1 && M > 128 && !patchk::takes_split_k(M, K, force)) {
@@ -1099,7 +1113,7 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
         for (int i = 0; i < count && same; ++i) same = Wps[i]->shp.K == K;
         if (same) {
             patchk::GemmLaunch gs[patchk::kDecMaxGroup];
-            for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X, M, Ys[i], y_is_fp32);
+            for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X, M, Ys[i], y_is_fp32, epi(i));
             patchk::DuoPlan dp;
             if (patchk::plan_hybrid_group(gs, count, &dp)) return from_cuda(patchk::launch_duo_group(gs, count, dp, stream));
         }
@@ -1110,13 +1124,13 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
     if (!one_launch) {
         // the products one after another on the stream (the same results)
         for (int i = 0; i < count; ++i) {
-            const patch_status st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, stream);
+            const patch_status st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream);
             if (st != PATCH_OK) return st;
         }
         return PATCH_OK;
     }
     patchk::GemmLaunch gs[patchk::kDecMaxGroup];
-    for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X, M, Ys[i], y_is_fp32);
+    for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X, M, Ys[i], y_is_fp32, epi(i));
     return from_cuda(patchk::launch_decode_group(gs, count, stream));
 }
 
@@ -1131,7 +1145,7 @@ patch_status patch_hybrid_gemm_group(const patch_packed *const *Wps, int32_t cou
         if (!Ys[i] || !aligned16(Ys[i])) return PATCH_ERR_INVALID_ARG;
     if (y_is_fp32 != 0 && y_is_fp32 != 1) return PATCH_ERR_INVALID_ARG;
     if (M > (int64_t(1) << 31)) return PATCH_ERR_INVALID_ARG;
-    return products(Wps, count, X_bf16, nullptr, M, Ys, y_is_fp32, static_cast<cudaStream_t>(stream_v));
+    return products(Wps, count, X_bf16, nullptr, M, Ys, y_is_fp32, nullptr, static_cast<cudaStream_t>(stream_v));
 }
 
 // -------------------------------------------- products with an epilogue
@@ -1168,26 +1182,68 @@ static patch_status check_epilogue(const patch_epilogue *epi, int64_t N, int64_t
     if (M > 0 && !Y) return PATCH_ERR_INVALID_ARG;
     // in place: every element is read and written by one thread, so the two must coincide
     if (Y && Y == e.residual && (ldy != ldr || y_is_fp32 != e.residual_is_fp32)) return PATCH_ERR_INVALID_ARG;
-    *out = patchk::Epilogue{e.bias, nullptr, e.residual, ldr, ldy, e.alpha, e.activation, e.bias_is_fp32,
-                            e.residual_is_fp32};
+    *out = patchk::Epilogue();
+    out->bias = e.bias;
+    out->residual = e.residual;
+    out->ldr = ldr;
+    out->ldy = ldy;
+    out->alpha = e.alpha;
+    out->act = e.activation;
+    out->bias_fp32 = e.bias_is_fp32;
+    out->res_fp32 = e.residual_is_fp32;
     return PATCH_OK;
 }
 
-// fp32 sums of every member in one pool block for the call, [M, N_i] each
-static patch_status sums_of(const patch_packed *const *Wps, int32_t count, const void *X, const float *x_scales,
-                            int64_t M, float **base, float **sums, cudaStream_t stream) {
-    size_t total = 0, off[patchk::kDecMaxGroup];
-    for (int i = 0; i < count; ++i) {
-        off[i] = total;
-        total = round_up(total + sizeof(float) * static_cast<size_t>(M) * static_cast<size_t>(Wps[i]->shp.N), 256);
+// The gated pair (arguments checked): one launch where the split-K or two-SM
+// kernels take both handles; otherwise the gate's activated values go to an
+// fp32 scratch that the up product's epilogue multiplies by.
+static patch_status gated_products(const patch_packed *const *hs, const void *X, const float *x_scales, int64_t M,
+                                   void *Y, int32_t y_is_fp32, const patchk::Epilogue &gate,
+                                   const patchk::Epilogue &up, cudaStream_t stream) {
+    const int64_t N = hs[0]->shp.N, K = hs[0]->shp.K;
+    const int force = g_test_kernel.load(std::memory_order_relaxed);
+    const bool same_sms = hs[0]->num_sms == hs[1]->num_sms;
+    const bool f8 = hs[0]->pattern == 8 && hs[1]->pattern == 8, bf = hs[0]->pattern == 2 && hs[1]->pattern == 2;
+    const patchk::Epilogue es[2] = {gate, up};
+    if (bf && same_sms) {
+        const patchk::GemmLaunch gs[2] = {gemm_launch(hs[0], X, M, Y, y_is_fp32, &es[0]),
+                                          gemm_launch(hs[1], X, M, Y, y_is_fp32, &es[1])};
+        if (patchk::takes_split_k(M, K, force)) return from_cuda(patchk::launch_decode_group(gs, 2, stream, true));
+        patchk::DuoPlan dp;
+        if (patchk::plan_hybrid_gated(gs, &dp)) return from_cuda(patchk::launch_duo_group(gs, 2, dp, stream, true));
     }
-    uint8_t *ws = nullptr;
-    const cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), total, Wps[0]->pool, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    *base = reinterpret_cast<float *>(ws);
-    void *ys[patchk::kDecMaxGroup];
-    for (int i = 0; i < count; ++i) ys[i] = sums[i] = reinterpret_cast<float *>(ws + off[i]);
-    return products(Wps, count, X, x_scales, M, ys, 1, stream);
+    XCodes x;
+    cudaError_t e = cudaSuccess;
+    if (f8) {
+        // X quantised once for both products, whichever kernels run
+        e = codes_of(hs[0], X, x_scales, M, &x, stream);
+        if (e != cudaSuccess) return free_codes(x, e, stream);
+        if (same_sms && force == 0 && M <= patchk::kDecodeMaxM && hs[0]->dec_nchunks > 0 && hs[1]->dec_nchunks > 0) {
+            const patchk::GemmLaunch gs[2] = {fp8_split_launch(hs[0], x.q, x.s, M, Y, y_is_fp32, &es[0]),
+                                              fp8_split_launch(hs[1], x.q, x.s, M, Y, y_is_fp32, &es[1])};
+            return free_codes(x, patchk::launch_decode_f8(gs, 2, stream, true), stream);
+        }
+        const patchk::Fp8Launch gs[2] = {fp8_launch(hs[0], x.q, x.s, M, Y, y_is_fp32, &es[0]),
+                                         fp8_launch(hs[1], x.q, x.s, M, Y, y_is_fp32, &es[1])};
+        patchk::DuoFp8Plan dp;
+        if (same_sms && patchk::takes_duo_fp8(gs[0]) && patchk::takes_duo_fp8(gs[1])) {
+            dp = patchk::plan_duo_fp8(N, M, gs[0].num_sms, gs[0].all_sparse && gs[1].all_sparse);
+            if (dp.bn > 0) return free_codes(x, patchk::launch_duo_fp8_group(gs, 2, dp, stream, true), stream);
+        }
+        X = x.q;
+        x_scales = x.s;
+    }
+    float *held = nullptr;
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&held), sizeof(float) * static_cast<size_t>(M * N),
+                                hs[0]->pool, stream);
+    if (e != cudaSuccess) return free_codes(x, e, stream);
+    patchk::Epilogue first = gate, second = up;
+    first.ldy = N;
+    second.mul = held;
+    patch_status st = product_one(hs[0], X, x_scales, M, held, 1, &first, stream);
+    if (st == PATCH_OK) st = product_one(hs[1], X, x_scales, M, Y, y_is_fp32, &second, stream);
+    const patch_status st2 = free_codes(x, cudaFreeAsync(held, stream), stream);
+    return st != PATCH_OK ? st : st2;
 }
 
 patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t count, const void *X,
@@ -1204,15 +1260,7 @@ patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t c
     }
     if (M == 0) return PATCH_OK;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-    float *base = nullptr, *sums[patchk::kDecMaxGroup];
-    st = sums_of(Wps, count, X, x_scales, M, &base, sums, stream);
-    for (int i = 0; i < count && st == PATCH_OK; ++i)
-        st = from_cuda(patchk::launch_epilogue(sums[i], nullptr, Ys[i], y_is_fp32, Wps[i]->shp.N, M, es[i], stream));
-    if (base) {
-        const cudaError_t e2 = cudaFreeAsync(base, stream);
-        if (st == PATCH_OK) st = from_cuda(e2);
-    }
-    return st;
+    return products(Wps, count, X, x_scales, M, Ys, y_is_fp32, es, stream);
 }
 
 patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
@@ -1233,18 +1281,13 @@ patch_status patch_hybrid_gated(const patch_packed *Wgate, const patch_packed *W
     st = check_epilogue(&pe, Wgate->shp.N, M, Y, y_is_fp32, &e);
     if (st != PATCH_OK) return st;
     if (!aligned_to(bias_up, real_bytes(bias_is_fp32))) return PATCH_ERR_INVALID_ARG;
-    e.bias2 = bias_up;
     if (M == 0) return PATCH_OK;
+    patchk::Epilogue up;
+    up.bias = bias_up;
+    up.bias_fp32 = bias_is_fp32;
+    up.ldy = e.ldy;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-    float *base = nullptr, *sums[2];
-    st = sums_of(hs, 2, X, x_scales, M, &base, sums, stream);
-    if (st == PATCH_OK)
-        st = from_cuda(patchk::launch_epilogue(sums[0], sums[1], Y, y_is_fp32, Wgate->shp.N, M, e, stream));
-    if (base) {
-        const cudaError_t e2 = cudaFreeAsync(base, stream);
-        if (st == PATCH_OK) st = from_cuda(e2);
-    }
-    return st;
+    return gated_products(hs, X, x_scales, M, Y, y_is_fp32, e, up, stream);
 }
 
 // ------------------------------------------------------- norms of a block

@@ -89,6 +89,20 @@ struct PlanArgs {
 constexpr int kStatusWords = 64;
 cudaError_t launch_plan_pack_group(const PlanArgs *args, int count, cudaStream_t stream);
 
+// What follows a product's sums (patch_epilogue of include/patch.h, strides
+// filled in): Y = residual + alpha * act(sum + bias), or, with `mul`,
+// Y = act(sum + bias) * mul.
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+struct Epilogue {
+    const void *bias = nullptr;      // [N]
+    const void *residual = nullptr;  // [M] rows ldr apart
+    const float *mul = nullptr;      // [M, N]
+    int64_t ldr = 0, ldy = 0;
+    float alpha = 1.0f;
+    int act = kActNone;
+    int bias_fp32 = 0, res_fp32 = 0;
+};
+
 struct GemmLaunch {
     const uint8_t *packed;
     const uint64_t *table;
@@ -119,6 +133,8 @@ struct GemmLaunch {
     // FP8 handles (split-K path only): X holds the e4m3 codes, Y = acc * sw[n] * sx[m]
     const float *f8_sw;      // [N] W_eff row scales
     const float *f8_sx;      // [M] token scales
+    int epi_on = 0;          // Y takes the epilogue `epi` (else the plain sums, rows of N)
+    Epilogue epi;
 };
 
 // Picks the configuration (token tile, schedule) for M and launches.
@@ -156,11 +172,17 @@ cudaError_t launch_duo_gemm(const GemmLaunch &g, const DuoPlan &plan, cudaStream
 // One launch over up to kDuoGroupMax matrices that read the same X (same K,
 // M and output type); the plan is made for the sum of their N.
 constexpr int kDuoGroupMax = 8;
-cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &plan, cudaStream_t stream);
+// `gated` as launch_decode_group; the plan is then made for one matrix's N.
+cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &plan, cudaStream_t stream,
+                             bool gated = false);
 // Whether one two-SM launch over the group (bf16 2:4 handles with paired
 // band types, the same X, more than 128 tokens) is estimated to finish before
 // the matrices' own launches one after another; fills *plan when it is.
 bool plan_hybrid_group(const GemmLaunch *gs, int count, DuoPlan *plan);
+// Whether one gated two-SM launch over the pair (one N, the same X, more than
+// 128 tokens) is estimated to finish no later than the two products one after
+// the other; fills *plan (made for one matrix's N) when it is.
+bool plan_hybrid_gated(const GemmLaunch *gs, DuoPlan *plan);
 double duo_kstep_cycles(int bn);
 
 // Two-SM, four-band prefill GEMM (csrc/prefill_quad.cu): each SM of a CTA
@@ -206,13 +228,15 @@ cudaError_t launch_decode_gemm(const GemmLaunch &g, cudaStream_t stream);
 // same X: the same K, M, X, output type and chunking; each member its own
 // handle fields and Y.  The first member's counter (and workspace, when large
 // enough) serve the launch.
-cudaError_t launch_decode_group(const GemmLaunch *gs, int count, cudaStream_t stream);
+// `gated` (count 2, one N, epilogues on): one output, gs[0].Y =
+// (act(sum_0 + bias_0)) * (sum_1 + bias_1), rows epi.ldy apart.
+cudaError_t launch_decode_group(const GemmLaunch *gs, int count, cudaStream_t stream, bool gated = false);
 // The same split-K kernel on FP8 handles (one matrix, or a group reading the
 // same X): 128-column e4m3 k-steps taken two per "pair", kind::f8f6f4 MMAs,
 // the fix-up applying each matrix's row scales and the token scales.  X holds
 // the e4m3 code matrix [M, K] (the same for every member, as is f8_sx),
 // M <= kDecodeMaxM.
-cudaError_t launch_decode_f8(const GemmLaunch *gs, int count, cudaStream_t stream);
+cudaError_t launch_decode_f8(const GemmLaunch *gs, int count, cudaStream_t stream, bool gated = false);
 // Chunking of a packed matrix for the decode GEMV: `cp` k-pairs per chunk,
 // `cpb` chunks per band.
 void plan_decode_chunks(int64_t bands, int64_t nsteps, int num_sms, int *cp, int *cpb, int *nchunks);
@@ -250,8 +274,12 @@ struct Fp8Launch {
     int num_sms;
     int force_kernel;        // test hook: 1 = one band per CTA, 3 = two-SM kernel, 0 = chosen here
     cudaMemPool_t pool;      // split-K partials of the one-band kernel (null: no split)
+    int epi_on = 0;          // as GemmLaunch
+    Epilogue epi;
 };
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream);
+// whether launch_fp8_gemm runs the two-SM kernel for this product
+bool takes_duo_fp8(const Fp8Launch &g);
 
 // Two-SM FP8 prefill GEMM (csrc/prefill_duo_fp8.cu): bands 2p, 2p+1 of the
 // prefill table on a CTA pair, two 128-column k-steps per stage.
@@ -269,25 +297,9 @@ cudaError_t launch_duo_fp8(const Fp8Launch &g, const DuoFp8Plan &plan, cudaStrea
 // One launch over up to kDuoGroupMax FP8 matrices that read the same X codes
 // and scales (same K, M and output type); the plan is made for the sum of
 // their N, with all_sparse only if every matrix is.
-cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Plan &plan, cudaStream_t stream);
-
-// What follows a product's sums (patch_epilogue of include/patch.h, resolved:
-// strides filled in).  The gated pair uses bias (gate), bias2 (up) and act.
-enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
-struct Epilogue {
-    const void *bias;      // [N] or null
-    const void *bias2;     // gated pair: the up product's bias, or null
-    const void *residual;  // [M] rows ldr apart, or null
-    int64_t ldr, ldy;
-    float alpha;
-    int act;
-    int bias_fp32, res_fp32;
-};
-// `up` null: Y = residual + alpha * act(sum + bias); else Y = act(sum + bias)
-// * (up + bias2).  sum and up are [M, N] fp32, N a multiple of 128.
-cudaError_t launch_epilogue(const float *sum, const float *up, void *Y, int y_fp32, int64_t N, int64_t M,
-                            const Epilogue &e, cudaStream_t stream);
-void preload_epilogue_kernels();
+// `gated` as launch_decode_group; the plan is then made for one matrix's N.
+cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Plan &plan, cudaStream_t stream,
+                                 bool gated = false);
 
 // Norms at the boundary of two sublayers (csrc/block_norm.cu); the fields of
 // patch_block_norm_args with the strides filled in.

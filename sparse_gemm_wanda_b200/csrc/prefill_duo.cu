@@ -41,6 +41,7 @@
 #include <mutex>
 
 #include "patch_cluster.cuh"
+#include "epilogue.cuh"
 #include "patch_common.cuh"
 #include "patch_internal.h"
 
@@ -77,6 +78,7 @@ struct DuoParams {
     int aslot;  // bytes of a stage's weight slot: the largest k-pair of the matrices
     int y_fp32;
     int stall_first_kstep;  // failure-detection test hook
+    Epilogue epi[kDuoMaxGroup];
 };
 
 // matrix holding global band pair gp
@@ -102,6 +104,7 @@ struct DuoMaps {
     CUtensorMap a_dd[kDuoMaxGroup], a_mixed[kDuoMaxGroup], a_ss[kDuoMaxGroup];
 };
 
+template <int MODE>
 __global__ void __launch_bounds__(kDuoThreads, 1)
 duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ DuoParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -128,13 +131,29 @@ duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ Du
     const int cl = blockIdx.x / 2, C = gridDim.x / 2;
     const int bn = p.bn, half = p.half;
 
-    auto fetch_table = [&](int item, int buf) {
-        const int gp = item / p.ttiles, mi = duo_mat_of_pair(p, gp);
-        const int band = 2 * (gp - p.pair0[mi]) + static_cast<int>(rank);
+    // Piece i of this cluster: the band pair bp of matrix mi and the token tile
+    // tt.  Gated: an item is the gate's band pair (piece 2q), then the same
+    // band pair of the up projection (piece 2q + 1).
+    auto locate = [&](int i, int &mi, int &bp, int &tt) {
+        const int item = cl + (MODE == kEpiGated ? i >> 1 : i) * C;
+        if (item >= p.items) return false;
+        const int gp = item / p.ttiles;
+        tt = item % p.ttiles;
+        mi = MODE == kEpiGated ? i & 1 : duo_mat_of_pair(p, gp);
+        bp = MODE == kEpiGated ? gp : gp - p.pair0[mi];
+        return true;
+    };
+    // piece i's table entries, if there is a piece i
+    auto fetch_table = [&](int i) {
+        int mi, bp, tt;
+        if (!locate(i, mi, bp, tt)) return false;
+        const int buf = i & 1;
+        const int band = 2 * bp + static_cast<int>(rank);
         const uint32_t nb = static_cast<uint32_t>(p.nsteps) * 8u;
         mbar_arrive_expect_tx(&tab_full[buf], nb);
         bulk_g2s(tab_buf + buf * kDuoTabSteps, p.table[mi] + static_cast<int64_t>(band) * p.nsteps, nb,
                  &tab_full[buf]);
+        return true;
     };
     auto give_up = [&]() {
         *abort_flag = 1u;
@@ -186,7 +205,8 @@ duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ Du
     // its peer at the end; the peer's waits then run out and it does the same
     const bool skip = *abort_flag != 0;
     if (threadIdx.x == 0 && !skip) {
-        for (int i = 0; i < 2 && cl + i * C < p.items; ++i) fetch_table(cl + i * C, i);
+        fetch_table(0);
+        fetch_table(1);
     }
 
     if (warp == 0) {
@@ -196,19 +216,18 @@ duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ Du
             int it = 0;
             bool ok = true;
             int tabs = 0;
-            for (int i = 0; i < 2 && cl + i * C < p.items; ++i) ++tabs;
+            int mi, bp, tt;
+            while (tabs < 2 && locate(tabs, mi, bp, tt)) ++tabs;
             // weights need no wait once the packer's ready flag was seen;
             // otherwise thread 0 already passed griddepcontrol.wait
             for (int i = 0; ok; ++i) {
-                const int item = cl + i * C;
-                if (item >= p.items) break;
+                if (!locate(i, mi, bp, tt)) break;
                 const int buf = i & 1;
                 if (!mbar_wait_bounded(&tab_full[buf], (i >> 1) & 1u, abort_flag, kDuoWaitLimitNs)) {
                     ok = false;
                     break;
                 }
                 const uint64_t *tab = tab_buf + buf * kDuoTabSteps;
-                const int mi = duo_mat_of_pair(p, item / p.ttiles);  // the item's matrix
                 for (int pr = 0; pr < p.nsteps / 2; ++pr) {
                     const int s = it % S;
                     const uint32_t ph = (it / S) & 1u;
@@ -236,10 +255,7 @@ duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ Du
                     tma2d_pair(smem + s * p.stage_bytes, am, 0, static_cast<int32_t>(first / 2048),
                                map_to_rank(&full[s], 0));
                 }
-                if (ok && cl + (i + 2) * C < p.items) {
-                    fetch_table(cl + (i + 2) * C, buf);
-                    ++tabs;
-                }
+                if (ok && fetch_table(i + 2)) ++tabs;
             }
             for (int q = (tabs > 2 ? tabs - 2 : 0); q < tabs; ++q)
                 mbar_wait_bounded(&tab_full[q & 1], (q >> 1) & 1u, never_flag, kDuoWaitLimitNs / 4);
@@ -265,9 +281,8 @@ duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ Du
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const int item = cl + i * C;
-                if (item >= p.items) break;
-                const int tt = item % p.ttiles;
+                int mi, bp, tt;
+                if (!locate(i, mi, bp, tt)) break;
                 for (int pr = 0; pr < p.nsteps / 2; ++pr) {
                     const int s = it % S;
                     const uint32_t ph = (it / S) & 1u;
@@ -303,8 +318,8 @@ duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ Du
             uint32_t ph = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const int item = cl + i * C;
-                if (item >= p.items) break;
+                int mi, bp, tt;
+                if (!locate(i, mi, bp, tt)) break;
                 const int buf = i & 1;
                 if (i >= 2 &&
                     !mbar_wait_bounded(&acc_empty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, kDuoWaitLimitNs)) {
@@ -360,23 +375,52 @@ duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ Du
         const int grp = warp >= 7 ? 1 : 0;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        // gated: the gate's activated values of this thread's columns, held from
+        // the first piece of an item to the second
+        [[maybe_unused]] uint32_t held[8][16];
         for (int i = 0;; ++i) {
-            const int item = cl + i * C;
-            if (item >= p.items) break;
-            const int gp = item / p.ttiles, tt = item % p.ttiles;
-            const int mi = duo_mat_of_pair(p, gp);
-            const int bp = gp - p.pair0[mi];
+            int mi, bp, tt;
+            if (!locate(i, mi, bp, tt)) break;
             const int buf = i & 1;
+            const int64_t n = static_cast<int64_t>(2 * bp + static_cast<int>(rank)) * kBand + row;
+            const int64_t m_base = static_cast<int64_t>(tt) * bn;
+            const int m_valid = static_cast<int>(min(static_cast<int64_t>(bn), p.M - m_base));
+            [[maybe_unused]] float bias = 0.0f;
+            if constexpr (MODE != kEpiPlain) bias = epi_bias(p.epi[mi], n);
+            // the first chunk's residual is read while the item's MMAs run
+            [[maybe_unused]] uint32_t add[16];
+            if constexpr (MODE == kEpiLinear)
+                epi_fetch(p.epi[mi], p.N[mi], m_base + 16 * grp, n, m_valid - 16 * grp, add);
             const bool ok = mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1u, never_flag, kDuoWaitLimitNs);
             tc_fence_after();
             if (!ok) {
                 give_up();
                 break;
             }
-            const int64_t n = static_cast<int64_t>(2 * bp + static_cast<int>(rank)) * kBand + row;
-            const int64_t m_base = static_cast<int64_t>(tt) * bn;
-            const int m_valid = static_cast<int>(min(static_cast<int64_t>(bn), p.M - m_base));
-            if (*abort_flag == 0) {
+            [[maybe_unused]] auto sums = [&](int c0, float (&v)[16]) {  // 16 columns of the accumulator
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * bn + c0), r);
+                tmem_ld_wait(r);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
+            };
+            if (*abort_flag != 0) {
+            } else if constexpr (MODE == kEpiLinear) {
+#pragma unroll 1
+                for (int c0 = 16 * grp; c0 < m_valid; c0 += 32) {
+                    float v[16];
+                    uint32_t next[16];
+                    sums(c0, v);
+                    // the next chunk's residual is on its way while this one is stored
+                    epi_fetch(p.epi[mi], p.N[mi], m_base + c0 + 32, n, m_valid - c0 - 32, next);
+                    epi_store(p.epi[mi], p.Y[mi], p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) add[q] = next[q];
+                }
+            } else if constexpr (MODE == kEpiGated) {
+                gated_piece(p.epi[mi], p.Y[0], p.y_fp32, mi, lane_base + static_cast<uint32_t>(buf * bn), grp,
+                            m_base, m_valid, n, bias, held, sums);
+            } else {
 #pragma unroll 1
                 for (int c0 = 16 * grp; c0 < m_valid; c0 += 32) {
                     uint32_t r[16];
@@ -437,8 +481,11 @@ cudaError_t ensure_duo_attributes() {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(duo_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kDuoSmemLimit);
+        for (auto *kernel : {duo_gemm_kernel<kEpiPlain>, duo_gemm_kernel<kEpiLinear>, duo_gemm_kernel<kEpiGated>}) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDuoSmemLimit);
+            if (e != cudaSuccess) attr_err = e;
+        }
     });
     return attr_err;
 }
@@ -462,7 +509,7 @@ int duo_max_clusters(int smem) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, duo_gemm_kernel, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, duo_gemm_kernel<kEpiPlain>, &cfg) != cudaSuccess) n = 0;
     cached_smem = smem;
     cached = n;
     return n;
@@ -478,7 +525,9 @@ double duo_kstep_cycles(int bn) {
 
 void preload_duo_kernels() {
     cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, duo_gemm_kernel);
+    (void)cudaFuncGetAttributes(&a, duo_gemm_kernel<kEpiPlain>);
+    (void)cudaFuncGetAttributes(&a, duo_gemm_kernel<kEpiLinear>);
+    (void)cudaFuncGetAttributes(&a, duo_gemm_kernel<kEpiGated>);
 }
 
 DuoPlan plan_duo_gemm(int64_t N, int64_t M, int num_sms, int max_pair_bytes) {
@@ -520,12 +569,13 @@ DuoPlan plan_duo_gemm(int64_t N, int64_t M, int num_sms, int max_pair_bytes) {
     return best;
 }
 
-cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &plan, cudaStream_t stream) {
+cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &plan, cudaStream_t stream, bool gated) {
     const cudaError_t attr_err = ensure_duo_attributes();
     if (attr_err != cudaSuccess) return attr_err;
     if (count < 1 || count > kDuoMaxGroup) return cudaErrorInvalidValue;
     if (plan.stages < 2 || plan.smem > kDuoSmemLimit || plan.clusters < 1) return cudaErrorInvalidValue;
     const GemmLaunch &g = gs[0];
+    if (gated && (count != 2 || gs[0].N != gs[1].N)) return cudaErrorInvalidValue;
     if (g.K / kStep > kDuoTabSteps) return cudaErrorInvalidValue;
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorInvalidValue;
@@ -546,8 +596,8 @@ cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &pla
     for (int i = 0; i < count; ++i) {
         const GemmLaunch &m = gs[i];
         // one X, one K, one output type; every matrix pairs its bands
-        if (m.K != g.K || m.M != g.M || m.X != g.X || m.y_fp32 != g.y_fp32 || (m.N / kBand) % 2 != 0 ||
-            !m.packed_rows || !m.ptable || !m.Y || !m.status || !m.ready)
+        if (m.K != g.K || m.M != g.M || m.X != g.X || m.y_fp32 != g.y_fp32 || m.epi_on != g.epi_on ||
+            (m.N / kBand) % 2 != 0 || !m.packed_rows || !m.ptable || !m.Y || !m.status || !m.ready)
             return cudaErrorInvalidValue;
         const uint64_t rows = m.packed_rows / 16;  // 2 KB rows
         if (!encode_rows(enc, &maps.a_dd[i], m.packed, rows, 2 * kDenseStepBytes / 2048) ||
@@ -558,6 +608,7 @@ cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &pla
         p.table[i] = m.ptable;  // the prefill table: the bands of every pair agree in type
         p.N[i] = m.N;
         p.Y[i] = m.Y;
+        p.epi[i] = m.epi;
         p.status[i] = m.status;
         p.ready[i] = m.ready;
         p.pair0[i] = static_cast<int32_t>(pairs);
@@ -580,7 +631,7 @@ cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &pla
     p.nsteps = static_cast<int>(g.K / kStep);
     p.ttiles = plan.ttiles;
     p.items = plan.items;
-    if (static_cast<int64_t>(p.items) != pairs * plan.ttiles) return cudaErrorInvalidValue;
+    if (static_cast<int64_t>(p.items) != (gated ? pairs / 2 : pairs) * plan.ttiles) return cudaErrorInvalidValue;
     p.bn = plan.bn;
     p.half = plan.bn / 2;
     p.stages = plan.stages;
@@ -603,7 +654,9 @@ cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &pla
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, duo_gemm_kernel, maps, p);
+    const cudaError_t err = gated      ? cudaLaunchKernelEx(&cfg, duo_gemm_kernel<kEpiGated>, maps, p)
+                            : g.epi_on ? cudaLaunchKernelEx(&cfg, duo_gemm_kernel<kEpiLinear>, maps, p)
+                                       : cudaLaunchKernelEx(&cfg, duo_gemm_kernel<kEpiPlain>, maps, p);
     if (err == cudaSuccess) note_launches(1);
     return err;
 }

@@ -41,6 +41,7 @@
 #include <mutex>
 
 #include "patch_cluster.cuh"
+#include "epilogue.cuh"
 #include "patch_common.cuh"
 #include "patch_internal.h"
 
@@ -78,6 +79,7 @@ struct D8Params {
     int bn, half, stages, stage_bytes, aslot;
     int aslot_step;          // weight bytes reserved per k-step in a stage (aslot = 2 x this)
     int y_fp32;
+    Epilogue epi[kD8MaxGroup];
 };
 
 // matrix holding global band pair gp
@@ -138,6 +140,7 @@ __device__ __forceinline__ void store_y(const D8Params &p, int mi, int64_t idx, 
         static_cast<__nv_bfloat16 *>(p.Y[mi])[idx] = __float2bfloat16_rn(v);
 }
 
+template <int MODE>
 __global__ void __launch_bounds__(kD8Threads, 1)
 duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -162,13 +165,29 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
     const int cl = blockIdx.x / 2, C = gridDim.x / 2;
     const int bn = p.bn, half = p.half;
 
-    auto fetch_table = [&](int item, int buf) {
-        const int gp = item / p.ttiles, mi = d8_mat_of_pair(p, gp);
-        const int band = 2 * (gp - p.pair0[mi]) + static_cast<int>(rank);
+    // Piece i of this cluster: the band pair bp of matrix mi and the token tile
+    // tt.  Gated: an item is the gate's band pair (piece 2q), then the same
+    // band pair of the up projection (piece 2q + 1).
+    auto locate = [&](int i, int &mi, int &bp, int &tt) {
+        const int item = cl + (MODE == kEpiGated ? i >> 1 : i) * C;
+        if (item >= p.items) return false;
+        const int gp = item / p.ttiles;
+        tt = item % p.ttiles;
+        mi = MODE == kEpiGated ? i & 1 : d8_mat_of_pair(p, gp);
+        bp = MODE == kEpiGated ? gp : gp - p.pair0[mi];
+        return true;
+    };
+    // piece i's table entries, if there is a piece i
+    auto fetch_table = [&](int i) {
+        int mi, bp, tt;
+        if (!locate(i, mi, bp, tt)) return false;
+        const int buf = i & 1;
+        const int band = 2 * bp + static_cast<int>(rank);
         const uint32_t nb = static_cast<uint32_t>(p.steps) * 8u;
         mbar_arrive_expect_tx(&tab_full[buf], nb);
         bulk_g2s(tab_buf + buf * kD8TabSteps, p.table[mi] + static_cast<int64_t>(band) * p.steps, nb,
                  &tab_full[buf]);
+        return true;
     };
     auto give_up = [&]() {
         *abort_flag = 1u;
@@ -214,7 +233,8 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
     const uint32_t tmem_base = *tmem_slot;
     const bool skip = *abort_flag != 0;
     if (threadIdx.x == 0 && !skip) {
-        for (int i = 0; i < 2 && cl + i * C < p.items; ++i) fetch_table(cl + i * C, i);
+        fetch_table(0);
+        fetch_table(1);
     }
     const int pairs = p.steps / 2;
 
@@ -224,17 +244,16 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
             int it = 0;
             bool ok = true;
             int tabs = 0;
-            for (int i = 0; i < 2 && cl + i * C < p.items; ++i) ++tabs;
+            int mi, bp, tt;
+            while (tabs < 2 && locate(tabs, mi, bp, tt)) ++tabs;
             for (int i = 0; ok; ++i) {
-                const int item = cl + i * C;
-                if (item >= p.items) break;
+                if (!locate(i, mi, bp, tt)) break;
                 const int buf = i & 1;
                 if (!mbar_wait_bounded(&tab_full[buf], (i >> 1) & 1u, abort_flag, kD8WaitLimitNs)) {
                     ok = false;
                     break;
                 }
                 const uint64_t *tab = tab_buf + buf * kD8TabSteps;
-                const int mi = d8_mat_of_pair(p, item / p.ttiles);  // the item's matrix
                 for (int pr = 0; pr < pairs; ++pr) {
                     const int s = it % S;
                     const uint32_t ph = (it / S) & 1u;
@@ -268,10 +287,7 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
                                    static_cast<int32_t>(f1 / 2048), map_to_rank(&full[s], 0));
                     }
                 }
-                if (ok && cl + (i + 2) * C < p.items) {
-                    fetch_table(cl + (i + 2) * C, buf);
-                    ++tabs;
-                }
+                if (ok && fetch_table(i + 2)) ++tabs;
             }
             for (int q = (tabs > 2 ? tabs - 2 : 0); q < tabs; ++q)
                 mbar_wait_bounded(&tab_full[q & 1], (q >> 1) & 1u, never_flag, kD8WaitLimitNs / 4);
@@ -293,9 +309,8 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const int item = cl + i * C;
-                if (item >= p.items) break;
-                const int tt = item % p.ttiles;
+                int mi, bp, tt;
+                if (!locate(i, mi, bp, tt)) break;
                 for (int pr = 0; pr < pairs; ++pr) {
                     const int s = it % S;
                     const uint32_t ph = (it / S) & 1u;
@@ -330,8 +345,8 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
             uint32_t ph = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const int item = cl + i * C;
-                if (item >= p.items) break;
+                int mi, bp, tt;
+                if (!locate(i, mi, bp, tt)) break;
                 const int buf = i & 1;
                 if (i >= 2 &&
                     !mbar_wait_bounded(&acc_empty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, kD8WaitLimitNs)) {
@@ -387,25 +402,57 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
         const int grp = warp >= 7 ? 1 : 0;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        // gated: the gate's activated values of this thread's columns, held from
+        // the first piece of an item to the second
+        [[maybe_unused]] uint32_t held[8][16];
         for (int i = 0;; ++i) {
-            const int item = cl + i * C;
-            if (item >= p.items) break;
-            const int gp = item / p.ttiles, tt = item % p.ttiles;
-            const int mi = d8_mat_of_pair(p, gp);
-            const int bp = gp - p.pair0[mi];
+            int mi, bp, tt;
+            if (!locate(i, mi, bp, tt)) break;
             const int buf = i & 1;
+            const int64_t n = static_cast<int64_t>(2 * bp + static_cast<int>(rank)) * kBand + row;
+            const int64_t m_base = static_cast<int64_t>(tt) * bn;
+            const int m_valid = static_cast<int>(min(static_cast<int64_t>(bn), p.M - m_base));
+            const float swn = __ldg(p.sw[mi] + n);
+            const int64_t ld = p.N[mi];
+            [[maybe_unused]] float bias = 0.0f;
+            if constexpr (MODE != kEpiPlain) bias = epi_bias(p.epi[mi], n);
+            // the first chunk's residual is read while the item's MMAs run
+            [[maybe_unused]] uint32_t add[16];
+            if constexpr (MODE == kEpiLinear)
+                epi_fetch(p.epi[mi], p.N[mi], m_base + 16 * grp, n, m_valid - 16 * grp, add);
             const bool ok = mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1u, never_flag, kD8WaitLimitNs);
             tc_fence_after();
             if (!ok) {
                 give_up();
                 break;
             }
-            const int64_t n = static_cast<int64_t>(2 * bp + static_cast<int>(rank)) * kBand + row;
-            const int64_t m_base = static_cast<int64_t>(tt) * bn;
-            const int m_valid = static_cast<int>(min(static_cast<int64_t>(bn), p.M - m_base));
-            const float swn = __ldg(p.sw[mi] + n);
-            const int64_t ld = p.N[mi];
-            if (*abort_flag == 0) {
+            // 16 columns of the accumulator with both scales applied
+            [[maybe_unused]] auto scaled = [&](int c0, float (&v)[16]) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * bn + c0), r);
+                const int ml = c0 + (lane & 15);
+                const float sxl = ml < m_valid ? __ldg(p.sx + m_base + ml) : 0.0f;
+                tmem_ld_wait(r);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]) * swn * __shfl_sync(0xFFFFFFFFu, sxl, q);
+            };
+            if (*abort_flag != 0) {
+            } else if constexpr (MODE == kEpiLinear) {
+#pragma unroll 1
+                for (int c0 = 16 * grp; c0 < m_valid; c0 += 32) {
+                    float v[16];
+                    uint32_t next[16];
+                    scaled(c0, v);
+                    // the next chunk's residual is on its way while this one is stored
+                    epi_fetch(p.epi[mi], p.N[mi], m_base + c0 + 32, n, m_valid - c0 - 32, next);
+                    epi_store(p.epi[mi], p.Y[mi], p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) add[q] = next[q];
+                }
+            } else if constexpr (MODE == kEpiGated) {
+                gated_piece(p.epi[mi], p.Y[0], p.y_fp32, mi, lane_base + static_cast<uint32_t>(buf * bn), grp,
+                            m_base, m_valid, n, bias, held, scaled);
+            } else {
 #pragma unroll 1
                 for (int c0 = 16 * grp; c0 < m_valid; c0 += 32) {
                     uint32_t r[16];
@@ -468,7 +515,11 @@ cudaError_t ensure_attributes() {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(duo_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kD8SmemLimit);
+        for (auto *kernel : {duo_fp8_kernel<kEpiPlain>, duo_fp8_kernel<kEpiLinear>, duo_fp8_kernel<kEpiGated>}) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kD8SmemLimit);
+            if (e != cudaSuccess) attr_err = e;
+        }
     });
     return attr_err;
 }
@@ -492,7 +543,7 @@ int max_clusters(int smem) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, duo_fp8_kernel, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, duo_fp8_kernel<kEpiPlain>, &cfg) != cudaSuccess) n = 0;
     cached_smem = smem;
     cached = n;
     return n;
@@ -502,7 +553,9 @@ int max_clusters(int smem) {
 
 void preload_duo_fp8_kernels() {
     cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, duo_fp8_kernel);
+    (void)cudaFuncGetAttributes(&a, duo_fp8_kernel<kEpiPlain>);
+    (void)cudaFuncGetAttributes(&a, duo_fp8_kernel<kEpiLinear>);
+    (void)cudaFuncGetAttributes(&a, duo_fp8_kernel<kEpiGated>);
 }
 
 DuoFp8Plan plan_duo_fp8(int64_t N, int64_t M, int num_sms, bool all_sparse) {
@@ -548,10 +601,12 @@ DuoFp8Plan plan_duo_fp8(int64_t N, int64_t M, int num_sms, bool all_sparse) {
     return best;
 }
 
-cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Plan &plan, cudaStream_t stream) {
+cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Plan &plan, cudaStream_t stream,
+                                 bool gated) {
     const cudaError_t attr_err = ensure_attributes();
     if (attr_err != cudaSuccess) return attr_err;
     if (count < 1 || count > kD8MaxGroup) return cudaErrorInvalidValue;
+    if (gated && (count != 2 || gs[0].N != gs[1].N)) return cudaErrorInvalidValue;
     const Fp8Launch &g = gs[0];
     const int64_t steps = g.K / kD8Step;
     if (plan.bn < 128 || plan.stages < 2 || plan.smem > kD8SmemLimit || plan.clusters < 1)
@@ -579,7 +634,7 @@ cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Pla
         const Fp8Launch &m = gs[i];
         // one X (codes and scales), one K, one output type; every matrix pairs its bands
         if (m.K != g.K || m.M != g.M || m.xq != g.xq || m.sx != g.sx || m.y_fp32 != g.y_fp32 ||
-            (m.N / kBand) % 2 != 0 || !m.ptable || !m.packed_bytes || !m.sw || !m.Y || !m.status)
+            m.epi_on != g.epi_on || (m.N / kBand) % 2 != 0 || !m.ptable || !m.packed_bytes || !m.sw || !m.Y || !m.status)
             return cudaErrorInvalidValue;
         // a matrix without dense k-steps only fits a plan sized for that
         if (!m.all_sparse && plan.aslot_step != kDenseStepBytes) return cudaErrorInvalidValue;
@@ -594,6 +649,7 @@ cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Pla
         p.sw[i] = m.sw;
         p.N[i] = m.N;
         p.Y[i] = m.Y;
+        p.epi[i] = m.epi;
         p.status[i] = m.status;
         p.pair0[i] = static_cast<int32_t>(pairs);
         pairs += m.N / (2 * kBand);
@@ -611,7 +667,7 @@ cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Pla
         p.status[i] = nullptr;
     }
     for (int i = count; i <= kD8MaxGroup; ++i) p.pair0[i] = static_cast<int32_t>(pairs);
-    if (static_cast<int64_t>(plan.items) != pairs * plan.ttiles) return cudaErrorInvalidValue;
+    if (static_cast<int64_t>(plan.items) != (gated ? pairs / 2 : pairs) * plan.ttiles) return cudaErrorInvalidValue;
     p.nmat = count;
     p.sx = g.sx;
     p.K = g.K;
@@ -639,7 +695,9 @@ cudaError_t launch_duo_fp8_group(const Fp8Launch *gs, int count, const DuoFp8Pla
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, duo_fp8_kernel, maps, p);
+    const cudaError_t err = gated      ? cudaLaunchKernelEx(&cfg, duo_fp8_kernel<kEpiGated>, maps, p)
+                            : g.epi_on ? cudaLaunchKernelEx(&cfg, duo_fp8_kernel<kEpiLinear>, maps, p)
+                                       : cudaLaunchKernelEx(&cfg, duo_fp8_kernel<kEpiPlain>, maps, p);
     if (err == cudaSuccess) note_launches(1);
     return err;
 }

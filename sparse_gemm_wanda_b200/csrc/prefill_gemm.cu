@@ -38,6 +38,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "epilogue.cuh"
 #include "patch_common.cuh"
 #include "patch_internal.h"
 
@@ -67,6 +68,7 @@ struct PairParams {
     uint32_t *status;
     const uint32_t *ready;
     int stall_first_kstep;  // failure-detection test hook
+    Epilogue epi;
 };
 
 __device__ __forceinline__ void store_y(const PairParams &p, int64_t idx, float v) {
@@ -81,6 +83,7 @@ __device__ __forceinline__ void tma_load_2d_x(void *dst, const void *tmap, int32
     tma_load_2d(dst, tmap, x, y, bar);
 }
 
+template <bool EPI>
 __global__ void __launch_bounds__(kPgThreads, 1)
 pair_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -346,7 +349,23 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
             const int64_t n = static_cast<int64_t>(2 * bp + j) * kBand + row;
             const int64_t m_base = static_cast<int64_t>(tt) * bn;
             const int m_valid = static_cast<int>(min(static_cast<int64_t>(bn), p.M - m_base));
-            if (live) {
+            if constexpr (EPI) {
+                if (live) {
+                    const float bias = epi_bias(p.epi, n);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < m_valid; c0 += 16) {
+                        uint32_t r[16];
+                        uint32_t add[16];
+                        float v[16];
+                        epi_fetch(p.epi, p.N, m_base + c0, n, m_valid - c0, add);
+                        tmem_ld_32x32b_x16(lane_base + c0, r);
+                        tmem_ld_wait(r);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
+                        epi_store(p.epi, p.Y, p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
+                    }
+                }
+            } else if (live) {
 #pragma unroll 1
                 for (int c0 = 0; c0 < m_valid; c0 += 16) {
                     uint32_t r[16];
@@ -393,7 +412,8 @@ double pair_kstep_cycles(int bn) { return 512.0 + 3.0 * bn; }
 
 void preload_pair_kernels() {
     cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, pair_gemm_kernel);
+    (void)cudaFuncGetAttributes(&a, pair_gemm_kernel<false>);
+    (void)cudaFuncGetAttributes(&a, pair_gemm_kernel<true>);
 }
 
 PairPlan plan_pair_gemm(int64_t N, int64_t M, int num_sms) {
@@ -430,8 +450,11 @@ cudaError_t launch_pair_gemm(const GemmLaunch &g, const PairPlan &plan, cudaStre
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(pair_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kPgSmemLimit);
+        for (auto *kernel : {pair_gemm_kernel<false>, pair_gemm_kernel<true>}) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgSmemLimit);
+            if (e != cudaSuccess) attr_err = e;
+        }
     });
     if (attr_err != cudaSuccess) return attr_err;
     if (plan.stages < 2 || plan.smem > kPgSmemLimit) return cudaErrorInvalidValue;
@@ -467,6 +490,7 @@ cudaError_t launch_pair_gemm(const GemmLaunch &g, const PairPlan &plan, cudaStre
     p.status = g.status;
     p.ready = g.ready;
     p.stall_first_kstep = g.stall_first_kstep;
+    p.epi = g.epi;
     if (p.nsteps > kPgTabSteps) return cudaErrorInvalidValue;
 
     cudaLaunchConfig_t cfg = {};
@@ -479,7 +503,8 @@ cudaError_t launch_pair_gemm(const GemmLaunch &g, const PairPlan &plan, cudaStre
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, pair_gemm_kernel, map, p);
+    const cudaError_t err = g.epi_on ? cudaLaunchKernelEx(&cfg, pair_gemm_kernel<true>, map, p)
+                                     : cudaLaunchKernelEx(&cfg, pair_gemm_kernel<false>, map, p);
     if (err == cudaSuccess) note_launches(1);
     return err;
 }
