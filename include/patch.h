@@ -486,10 +486,10 @@ typedef struct {
 
 /*
  * Hybrid product with an epilogue: Y = residual + alpha * act(X W_eff^T + bias).
- * The sums are exactly patch_hybrid_gemm's (for FP8 handles with both scales
- * applied); the epilogue is computed on them in fp32 and the result is
- * rounded once to Y's type, so no product is stored before it is activated
- * and added.
+ * The sums are patch_hybrid_gemm's up to fp32 rounding order (the kernel may
+ * be another one), for FP8 handles with both scales applied; the epilogue is
+ * computed on them in fp32 and the result is rounded once to Y's type, so no
+ * product is stored before it is activated and added.
  *
  *   Wp        handle from any of the pack calls, of the current device.
  *   X         x_scales NULL: bf16 [M,K] as patch_hybrid_gemm (FP8 handles
@@ -532,7 +532,7 @@ patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t c
 
 /*
  * The gated pair of an MLP: Y = act(X W_gate^T + bias_gate) * (X W_up^T + bias_up),
- * both products' sums as patch_hybrid_gemm's, the rest in fp32, one rounding.
+ * both products' sums as patch_hybrid_linear's, the rest in fp32, one rounding.
  *
  *   Wgate, Wup  handles of the same N and K (any kinds), current device.
  *   X, x_scales, M  as patch_hybrid_linear (x_scales: both handles FP8).

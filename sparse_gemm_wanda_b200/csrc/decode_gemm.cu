@@ -53,6 +53,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <iterator>
 #include <mutex>
 
 #include "epilogue.cuh"
@@ -123,13 +124,8 @@ struct DecodeParams {
     int32_t band0[kDecMaxGroup + 1];
     const uint8_t *packed[kDecMaxGroup];
     const uint64_t *chunk_desc[kDecMaxGroup];  // [bands * cpb] of each matrix
-    void *Y[kDecMaxGroup];
-    int64_t N[kDecMaxGroup];
     uint32_t *status[kDecMaxGroup];
     const uint32_t *ready[kDecMaxGroup];
-    int y_fp32;
-    const float *f8_sw[kDecMaxGroup];  // FP8: [N] row scales of each matrix
-    const float *f8_sx;                // FP8: [M] token scales (the shared X)
     float *partial[kDecMaxGroup];  // per matrix: [its chunks][BN][128]
     uint32_t *counter;  // chunks claimed beyond the first 2 * gridDim.x; zero between calls
     int stall_first_kstep;  // failure-detection test hook
@@ -137,13 +133,23 @@ struct DecodeParams {
     uint64_t second_desc[kDecMaxCtas];  // of chunk c + gridDim.x where that exists
 };
 
-// the matrices' epilogues, for the fix-up only
-struct DecodeEpi {
-    Epilogue e[kDecMaxGroup];
+// What the fix-up needs: the partials and the outputs, each matrix with its epilogue.
+struct ReduceParams {
+    int cpb, nmat;
+    int32_t band0[kDecMaxGroup + 1];
+    int y_fp32;
+    const float *partial[kDecMaxGroup];
+    void *Y[kDecMaxGroup];
+    int64_t N[kDecMaxGroup];
+    const float *f8_sw[kDecMaxGroup];  // FP8: [N] row scales of each matrix
+    const float *f8_sx;                // FP8: [M] token scales (the shared X)
+    uint32_t *counter;
+    Epilogue epi[kDecMaxGroup];
 };
 
 // matrix holding global band gb
-__device__ __forceinline__ int dec_mat_of_band(const DecodeParams &p, int gb) {
+template <class Params>
+__device__ __forceinline__ int dec_mat_of_band(const Params &p, int gb) {
     int i = 0;
     while (i + 1 < p.nmat && p.band0[i + 1] <= gb) ++i;
     return i;
@@ -188,13 +194,6 @@ __device__ __forceinline__ bool wait_count_bounded(volatile uint32_t *ctr, uint3
             if (globaltimer_ns() - t0 > limit_ns) return false;
         }
     }
-}
-
-__device__ __forceinline__ void store_out(const DecodeParams &p, int mi, int64_t idx, float v) {
-    if (p.y_fp32)
-        static_cast<float *>(p.Y[mi])[idx] = v;
-    else
-        static_cast<__nv_bfloat16 *>(p.Y[mi])[idx] = __float2bfloat16_rn(v);
 }
 
 template <int BN, bool F8>
@@ -571,7 +570,7 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 
 // The partials of one output added in chunk order, from zero; FP8: times both scales.
 template <int BN, bool F8>
-__device__ __forceinline__ float dec_sum(const DecodeParams &p, int mi, int band, int m, int row) {
+__device__ __forceinline__ float dec_sum(const ReduceParams &p, int mi, int band, int m, int row) {
     const float *src = p.partial[mi] + (static_cast<int64_t>(band) * p.cpb * BN + m) * kBand + row;
     float acc = 0.0f;
     for (int c0 = 0; c0 < p.cpb; c0 += 8) {
@@ -595,7 +594,7 @@ __device__ __forceinline__ float dec_sum(const DecodeParams &p, int mi, int band
 // once the GEMM is complete.
 template <int BN, bool F8, int MODE>
 __global__ void __launch_bounds__(kBand)
-decode_reduce_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ DecodeEpi epi) {
+decode_reduce_kernel(const __grid_constant__ ReduceParams p) {
     if (threadIdx.x == 0) pdl_trigger();  // the next GEMM may start its prologue
     pdl_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.counter = 0u;
@@ -604,9 +603,9 @@ decode_reduce_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     const int band = blockIdx.x - p.band0[mi];
     const int64_t n = static_cast<int64_t>(band) * kBand + row;
     if constexpr (MODE == kEpiPlain) {
-        store_out(p, mi, static_cast<int64_t>(m) * p.N[mi] + n, dec_sum<BN, F8>(p, mi, band, m, row));
+        store_real(p.Y[mi], static_cast<int64_t>(m) * p.N[mi] + n, dec_sum<BN, F8>(p, mi, band, m, row), p.y_fp32);
     } else {
-        const Epilogue &e = epi.e[mi];
+        const Epilogue &e = p.epi[mi];
         float v[1];
         const float b = epi_bias(e, n);
         if constexpr (MODE == kEpiLinear) {
@@ -615,7 +614,7 @@ decode_reduce_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             v[0] = dec_sum<BN, F8>(p, mi, band, m, row);
             epi_store(e, p.Y[mi], p.y_fp32, m, n, 1, b, v, r);
         } else {
-            const float u = dec_sum<BN, F8>(p, 1, band, m, row) + epi_bias(epi.e[1], n);
+            const float u = dec_sum<BN, F8>(p, 1, band, m, row) + epi_bias(p.epi[1], n);
             v[0] = dec_sum<BN, F8>(p, 0, band, m, row) + b;
             activate(v, e.act);
             store_real(p.Y[0], static_cast<int64_t>(m) * e.ldy + n, v[0] * u, p.y_fp32);
@@ -708,24 +707,24 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, 
     if (!g.counter) return cudaErrorInvalidValue;
     if (g.dec_cp < 1 || g.dec_cp > kDecChunkPairs || g.dec_cpb < 1) return cudaErrorInvalidValue;
 
-    DecodeEpi epi;
+    ReduceParams r;
     DecodeParams p;
     p.K = g.K;
     p.M = g.M;
     p.cpb = g.dec_cpb;
     p.cp = g.dec_cp;
     p.nmat = count;
-    p.y_fp32 = g.y_fp32;
-    p.f8_sx = g.f8_sx;
+    r.y_fp32 = g.y_fp32;
+    r.f8_sx = g.f8_sx;
     p.counter = g.counter;
     p.stall_first_kstep = g.stall_first_kstep;
     int64_t bands = 0;
     for (int i = 0; i < kDecMaxGroup; ++i) {
         p.packed[i] = nullptr;
-        p.f8_sw[i] = nullptr;
+        r.f8_sw[i] = nullptr;
         p.chunk_desc[i] = nullptr;
-        p.Y[i] = nullptr;
-        p.N[i] = 0;
+        r.Y[i] = nullptr;
+        r.N[i] = 0;
         p.status[i] = nullptr;
         p.ready[i] = nullptr;
     }
@@ -739,11 +738,11 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, 
             return cudaErrorInvalidValue;
         p.band0[i] = static_cast<int32_t>(bands);
         p.packed[i] = m.packed;
-        p.f8_sw[i] = m.f8_sw;
+        r.f8_sw[i] = m.f8_sw;
         p.chunk_desc[i] = m.chunk_desc;
-        p.Y[i] = m.Y;
-        epi.e[i] = m.epi;
-        p.N[i] = m.N;
+        r.Y[i] = m.Y;
+        r.N[i] = m.N;
+        r.epi[i] = m.epi;
         p.status[i] = m.status;
         p.ready[i] = m.ready;
         bands += m.N / kBand;
@@ -799,9 +798,14 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, 
         cfg.gridDim = dim3(static_cast<unsigned>(gated ? g.N / kBand : bands), static_cast<unsigned>(g.M));
         cfg.blockDim = dim3(kBand);
         cfg.dynamicSmemBytes = 0;
-        err = gated      ? cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiGated>, p, epi)
-              : g.epi_on ? cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiLinear>, p, epi)
-                         : cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiPlain>, p, epi);
+        r.cpb = p.cpb;
+        r.nmat = p.nmat;
+        r.counter = p.counter;
+        std::copy(std::begin(p.band0), std::end(p.band0), r.band0);
+        std::copy(std::begin(p.partial), std::end(p.partial), r.partial);
+        err = gated      ? cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiGated>, r)
+              : g.epi_on ? cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiLinear>, r)
+                         : cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiPlain>, r);
         if (err == cudaSuccess) note_launches(1);
     }
     if (ws) {

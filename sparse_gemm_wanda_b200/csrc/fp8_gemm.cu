@@ -399,6 +399,22 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// At most half as many tiles as SMs: split each tile's k-steps so that about
+// two work items fall on every SM (ranges of equal length, none empty); with
+// more tiles the partials and the fix-up cost more than the idle SMs (measured
+// on 11008x4096: 86 tiles, 22.3 us split against 17.3).
+void split_tiles(const Fp8Launch &g, int tiles, int steps, int *ksplit, int *kper) {
+    *ksplit = 1;
+    *kper = steps;
+    if (2 * tiles <= g.num_sms && g.pool) {
+        const int want = std::min(steps, std::min(16, (2 * g.num_sms + tiles - 1) / tiles));
+        if (want > 1) {
+            *kper = (steps + want - 1) / want;
+            *ksplit = (steps + *kper - 1) / *kper;
+        }
+    }
+}
+
 template <int BN, bool EPI>
 cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     using C = F8Cfg<BN>;
@@ -438,19 +454,7 @@ cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     p.y_fp32 = g.y_fp32;
     p.status = g.status;
     p.epi = g.epi;
-    // at most half as many tiles as SMs: split each tile's k-steps so that
-    // about two work items fall on every SM (ranges of equal length, none
-    // empty); with more tiles the partials and the fix-up cost more than the
-    // idle SMs (measured on 11008x4096: 86 tiles, 22.3 us split against 17.3)
-    p.ksplit = 1;
-    p.kper = p.steps;
-    if (2 * p.tiles <= g.num_sms && g.pool) {
-        const int want = std::min(p.steps, std::min(16, (2 * g.num_sms + p.tiles - 1) / p.tiles));
-        if (want > 1) {
-            p.kper = (p.steps + want - 1) / want;
-            p.ksplit = (p.steps + p.kper - 1) / p.kper;
-        }
-    }
+    split_tiles(g, p.tiles, p.steps, &p.ksplit, &p.kper);
     p.items = p.tiles * p.ksplit;
     p.partial = nullptr;
     float *ws = nullptr;
@@ -515,11 +519,63 @@ void preload_fp8_gemm_kernels() {
     preload_fp8<240, true>();
 }
 
+namespace {
+
+// the two-SM kernel: the bands pair up (prefill table), an even k-step count
+bool duo_fits(const Fp8Launch &g) {
+    return g.ptable && (g.N / kBand) % 2 == 0 && (g.K / kF8Step) % 2 == 0 && g.K / kF8Step <= 224 &&
+           g.force_kernel != 1;
+}
+
+// Estimated time (us) of one product of more than 64 tokens with an epilogue
+// on the one-band kernel with its partials; duo_fp8_us the two-SM kernel's
+// (`pieces` of it a work item).  Fitted to calls in a graph on B200, f = 0.5, X quantised (us,
+// one-band / two-SM): 256x8192 M = 129 10.6 / 26.7, 1024x8192 M = 300 18.1 /
+// 28.5, 512x4096 M = 512 15.9 / 20.7, 4096x4096 M = 300 33.5 / 20.4,
+// 2048x1024 M = 512 22.1 / 14.0, M = 1024 20.2 / 14.9.
+double one_band_fp8_us(const Fp8Launch &g) {
+    const int bn = g.M <= 128 ? 128 : 240;
+    const int64_t tiles = (g.N / kBand) * ((g.M + bn - 1) / bn);
+    if (tiles > 1 << 24) return 1e9;
+    int ksplit, kper;
+    split_tiles(g, static_cast<int>(tiles), static_cast<int>(g.K / kF8Step), &ksplit, &kper);
+    const int64_t rounds = (tiles * ksplit + g.num_sms - 1) / g.num_sms;
+    const double partial_mb = ksplit > 1 ? 4e-6 * static_cast<double>(g.M) * static_cast<double>(g.N) * ksplit : 0.0;
+    // unsplit, a tile's own epilogue: four warps storing bn columns
+    const double store = ksplit > 1 ? 0.0 : static_cast<double>(rounds * bn) / 30.0;
+    return 8.5 + 0.45 * static_cast<double>(rounds * kper) + partial_mb / 3.0 + store;
+}
+
+}  // namespace
+
+double duo_fp8_us(const Fp8Launch &g, const DuoFp8Plan &dp, int pieces) {
+    return 11.0 + pieces * dp.cost * static_cast<double>(g.K / kF8Step) / 1750.0;
+}
+
 bool takes_duo_fp8(const Fp8Launch &g) {
-    // more than one token tile: the two-SM kernel, where the bands pair up
-    // (prefill table) and the k-step count is even
-    const bool duo_ok = g.ptable && (g.N / kBand) % 2 == 0 && (g.K / kF8Step) % 2 == 0 && g.K / kF8Step <= 224;
-    return duo_ok && g.force_kernel != 1 && (g.M > 128 || g.force_kernel == 3);
+    if (!duo_fits(g)) return false;
+    if (g.force_kernel == 3) return true;
+    // plain products: whenever there is more than one token tile
+    if (!g.epi_on) return g.M > 128;
+    if (g.M <= 64) return false;
+    const DuoFp8Plan dp = plan_duo_fp8(g.N, g.M, g.num_sms, g.all_sparse != 0);
+    return dp.bn > 0 && duo_fp8_us(g, dp, 1) <= one_band_fp8_us(g);
+}
+
+double fp8_us(const Fp8Launch &g) {
+    const double one = one_band_fp8_us(g);
+    if (!duo_fits(g)) return one;
+    const DuoFp8Plan dp = plan_duo_fp8(g.N, g.M, g.num_sms, g.all_sparse != 0);
+    return dp.bn > 0 ? std::min(one, duo_fp8_us(g, dp, 1)) : one;
+}
+
+bool takes_duo_fp8_gated(const Fp8Launch *gs) {
+    const Fp8Launch &g = gs[0];
+    if (!duo_fits(gs[0]) || !duo_fits(gs[1])) return false;
+    if (g.force_kernel == 3) return true;
+    if (g.M <= 64) return false;
+    const DuoFp8Plan dp = plan_duo_fp8(g.N, g.M, g.num_sms, gs[0].all_sparse && gs[1].all_sparse);
+    return dp.bn > 0 && duo_fp8_us(g, dp, 2) <= fp8_us(gs[0]) + fp8_us(gs[1]);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream) {

@@ -831,6 +831,56 @@ void preload_hybrid_kernels() {
     preload_modes<true>();
 }
 
+namespace {
+
+// Kernel and estimated time (us) of one bf16 2:4 product of more than 64
+// tokens with an epilogue.  The wave counts alone (launch_hybrid_gemm's rule
+// for plain products, kept there with their results) miss what a call costs
+// before its first and after its last k-step, and that the one-band kernel
+// spreads few tiles over every SM.  Fitted to calls in a graph on B200, f = 0.5
+// (us, one-band / two-SM): 256x8192 M = 129 15.3 / 35.9, 1024x8192 M = 512
+// 23.8 / 36.5, 512x4096 M = 300 15.1 / 21.3, 1024x2048 M = 300 16.2 / 13.9,
+// 4096x1024 M = 100 15.4 / 9.9, 4096x4096 M = 100 18.2 / 21.2, M = 200 27.9 /
+// 21.6; band-pair 4096x4096 M = 129 48.7, 4096x1024 M = 300 21.4.
+struct Choice {
+    int kernel = 1;  // 1 one band, 2 band pair, 3 two-SM
+    double us = 0;
+    DuoPlan duo{};
+    PairPlan pair{};
+};
+constexpr double kCyclesPerUs = 1750.0;
+
+double duo_us(const DuoPlan &dp, int64_t K, int pieces) {
+    return 6.3 + pieces * dp.cost * static_cast<double>(K / kStep) / kCyclesPerUs;
+}
+
+Choice choose_kernel(const GemmLaunch &g) {
+    Choice c;
+    const int64_t bn = g.M <= 128 ? 128 : 160;
+    const int64_t units = (g.N / kBand) * ((g.M + bn - 1) / bn) * (g.K / (2 * kStep));
+    c.us = (bn == 128 ? 10.5 : 11.5) + static_cast<double>((units + g.num_sms - 1) / g.num_sms) +
+           (bn == 128 ? 2e-6 : 6e-6) * static_cast<double>(g.M) * static_cast<double>(g.N);
+    if (g.K / kStep > 448) return c;
+    if (g.duo_ok) {
+        const DuoPlan dp = plan_duo_gemm(g.N, g.M, g.num_sms, g.max_pair_bytes);
+        if (dp.bn > 0 && duo_us(dp, g.K, 1) < c.us) {
+            c.kernel = 3;
+            c.us = duo_us(dp, g.K, 1);
+            c.duo = dp;
+        }
+    }
+    const PairPlan pp = plan_pair_gemm(g.N, g.M, g.num_sms);
+    const double us = 12.0 + pp.cost * static_cast<double>(g.K / kStep) / 2100.0;
+    if (us < c.us) {
+        c.kernel = 2;
+        c.us = us;
+        c.pair = pp;
+    }
+    return c;
+}
+
+}  // namespace
+
 cudaError_t launch_hybrid_gemm(const GemmLaunch &g, cudaStream_t stream) {
     if (g.pattern == 4) {
         // 4:8 handles: the one-band kernel with converter warps, every M
@@ -860,6 +910,12 @@ cudaError_t launch_hybrid_gemm(const GemmLaunch &g, cudaStream_t stream) {
     // against 20.6 / 21.2.
     if (takes_split_k(g.M, g.K, 0)) return launch_decode_gemm(g, stream);
     if (g.M <= 64) return run<64, 4>(g, 1, stream);   // 48 KB stages
+    if (g.epi_on) {
+        const Choice c = choose_kernel(g);
+        if (c.kernel == 3) return launch_duo_gemm(g, c.duo, stream);
+        if (c.kernel == 2) return launch_pair_gemm(g, c.pair, stream);
+        return g.M <= 128 ? run<128, 3>(g, 1, stream) : run<160, 3>(g, 1, stream);
+    }
     if (g.M <= 128) return run<128, 3>(g, 1, stream); // 64 KB stages
     // larger token counts: the band-pair kernel (two bands share each X tile)
     // unless its items fall into so few waves that this kernel's finer tiles
@@ -905,10 +961,10 @@ double own_prefill_cost(const GemmLaunch &g) {
 bool plan_hybrid_group(const GemmLaunch *gs, int count, DuoPlan *plan) {
     if (count < 2 || count > kDuoGroupMax) return false;
     const GemmLaunch &g = gs[0];
-    if (g.M <= 128 || g.K / kStep > 448) return false;
+    if (g.M <= (g.epi_on ? 64 : 128) || g.K / kStep > 448) return false;
     int64_t sum_n = 0;
     int max_pair = 0;
-    double own = 0;
+    double own = 0, own_us = 0;
     for (int i = 0; i < count; ++i) {
         const GemmLaunch &m = gs[i];
         if (m.pattern != 2 || !m.duo_ok || m.K != g.K || m.M != g.M || m.num_sms != g.num_sms ||
@@ -916,26 +972,29 @@ bool plan_hybrid_group(const GemmLaunch *gs, int count, DuoPlan *plan) {
             return false;
         sum_n += m.N;
         max_pair = std::max(max_pair, m.max_pair_bytes);
-        own += own_prefill_cost(m);
+        if (g.epi_on)
+            own_us += choose_kernel(m).us;
+        else
+            own += own_prefill_cost(m);
     }
     // test hook 3 (two-SM kernel for every M) takes the grouped launch too
     if (g.force_kernel != 0 && g.force_kernel != 3) return false;
     const DuoPlan dp = plan_duo_gemm(sum_n, g.M, g.num_sms, max_pair);
     if (dp.bn == 0) return false;
-    if (g.force_kernel == 0 && dp.cost > own) return false;
+    if (g.force_kernel == 0 && (g.epi_on ? duo_us(dp, g.K, 1) > own_us : dp.cost > own)) return false;
     *plan = dp;
     return true;
 }
 
 bool plan_hybrid_gated(const GemmLaunch *gs, DuoPlan *plan) {
     const GemmLaunch &g = gs[0];
-    if (g.M <= 128 && g.force_kernel != 3) return false;
+    if (g.M <= 64 && g.force_kernel != 3) return false;
     if (g.force_kernel != 0 && g.force_kernel != 3) return false;
     if (!gs[0].duo_ok || !gs[1].duo_ok || g.K / kStep > 448) return false;
     // an item is both matrices' band pair: twice the k-steps of one product
     const DuoPlan dp = plan_duo_gemm(g.N, g.M, g.num_sms, std::max(gs[0].max_pair_bytes, gs[1].max_pair_bytes));
     if (dp.bn == 0) return false;
-    if (g.force_kernel == 0 && 2 * dp.cost > own_prefill_cost(gs[0]) + own_prefill_cost(gs[1])) return false;
+    if (g.force_kernel == 0 && duo_us(dp, g.K, 2) > choose_kernel(gs[0]).us + choose_kernel(gs[1]).us) return false;
     *plan = dp;
     return true;
 }

@@ -1072,7 +1072,7 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
         for (int i = 0; i < count; ++i) gs[i] = fp8_split_launch(Wps[i], x.q, x.s, M, Ys[i], y_is_fp32, epi(i));
         return free_codes(x, patchk::launch_decode_f8(gs, count, stream), stream);
     }
-    if (count > 1 && M > 128 && (force == 0 || force == 3)) {
+    if (count > 1 && M > (epis ? 64 : 128) && (force == 0 || force == 3)) {
         // FP8 prefill: X quantised once, then one two-SM launch over every
         // matrix's band pairs when the estimate says it finishes first
         const int64_t steps = K / 128;
@@ -1090,11 +1090,16 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
             sum_n += h->shp.N;
             const patchk::DuoFp8Plan one = patchk::plan_duo_fp8(h->shp.N, M, h->num_sms, sp);
             ok = one.bn > 0;
-            own += one.cost;
+            // with epilogues the kernels are chosen by estimated times
+            own += epis ? patchk::fp8_us(fp8_launch(h, nullptr, nullptr, M, nullptr, 0, epi(i))) : one.cost;
         }
         patchk::DuoFp8Plan dp{};
         if (ok) dp = patchk::plan_duo_fp8(sum_n, M, Wps[0]->num_sms, all_sparse);
-        if (ok && dp.bn > 0 && (force == 3 || dp.cost <= own)) {
+        auto cost = [&] {
+            if (!epis) return dp.cost;
+            return patchk::duo_fp8_us(fp8_launch(Wps[0], nullptr, nullptr, M, nullptr, 0, epi(0)), dp, 1);
+        };
+        if (ok && dp.bn > 0 && (force == 3 || cost() <= own)) {
             XCodes x;
             cudaError_t e = codes_of(Wps[0], X, x_scales, M, &x, stream);
             if (e == cudaSuccess) {
@@ -1105,7 +1110,7 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
             return free_codes(x, e, stream);
         }
     }
-    if (count > 1 && M > 128 && !patchk::takes_split_k(M, K, force)) {
+    if (count > 1 && M > (epis ? 64 : 128) && !patchk::takes_split_k(M, K, force)) {
         // prefill: one two-SM launch over every matrix's band pairs when the
         // estimate says it finishes first (fills the SMs that one matrix's
         // items leave idle in its last wave)
@@ -1226,7 +1231,7 @@ static patch_status gated_products(const patch_packed *const *hs, const void *X,
         const patchk::Fp8Launch gs[2] = {fp8_launch(hs[0], x.q, x.s, M, Y, y_is_fp32, &es[0]),
                                          fp8_launch(hs[1], x.q, x.s, M, Y, y_is_fp32, &es[1])};
         patchk::DuoFp8Plan dp;
-        if (same_sms && patchk::takes_duo_fp8(gs[0]) && patchk::takes_duo_fp8(gs[1])) {
+        if (same_sms && patchk::takes_duo_fp8_gated(gs)) {
             dp = patchk::plan_duo_fp8(N, M, gs[0].num_sms, gs[0].all_sparse && gs[1].all_sparse);
             if (dp.bn > 0) return free_codes(x, patchk::launch_duo_fp8_group(gs, 2, dp, stream, true), stream);
         }
@@ -1335,7 +1340,7 @@ patch_status patch_block_norm(const patch_block_norm_args *a, int64_t M, int64_t
     if (!a->branch || (!a->h && a->z_type == PATCH_Z_NONE) || (a->z_type != PATCH_Z_NONE && !a->z) ||
         (a->z && a->z_type == PATCH_Z_NONE) || (e4m3 && !a->z_scales))
         return PATCH_ERR_INVALID_ARG;
-    const patch_status st = check_device(nullptr);
+    const patch_status st = check_device(&p.num_sms);
     if (st != PATCH_OK) return st;
     p.branch = a->branch;
     p.residual = a->residual;

@@ -180,7 +180,7 @@ cudaError_t launch_duo_group(const GemmLaunch *gs, int count, const DuoPlan &pla
 // the matrices' own launches one after another; fills *plan when it is.
 bool plan_hybrid_group(const GemmLaunch *gs, int count, DuoPlan *plan);
 // Whether one gated two-SM launch over the pair (one N, the same X, more than
-// 128 tokens) is estimated to finish no later than the two products one after
+// 64 tokens) is estimated to finish no later than the two products one after
 // the other; fills *plan (made for one matrix's N) when it is.
 bool plan_hybrid_gated(const GemmLaunch *gs, DuoPlan *plan);
 double duo_kstep_cycles(int bn);
@@ -280,6 +280,9 @@ struct Fp8Launch {
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream);
 // whether launch_fp8_gemm runs the two-SM kernel for this product
 bool takes_duo_fp8(const Fp8Launch &g);
+// whether one two-SM launch is estimated to finish a gated pair no later than
+// two products one after another
+bool takes_duo_fp8_gated(const Fp8Launch *gs);
 
 // Two-SM FP8 prefill GEMM (csrc/prefill_duo_fp8.cu): bands 2p, 2p+1 of the
 // prefill table on a CTA pair, two 128-column k-steps per stage.
@@ -294,6 +297,10 @@ struct DuoFp8Plan {
 };
 DuoFp8Plan plan_duo_fp8(int64_t N, int64_t M, int num_sms, bool all_sparse);
 cudaError_t launch_duo_fp8(const Fp8Launch &g, const DuoFp8Plan &plan, cudaStream_t stream);
+// Estimated times (us) of products of more than 64 tokens with an epilogue:
+// one two-SM launch, and one product on whichever kernel is estimated fastest.
+double duo_fp8_us(const Fp8Launch &g, const DuoFp8Plan &dp, int pieces);
+double fp8_us(const Fp8Launch &g);
 // One launch over up to kDuoGroupMax FP8 matrices that read the same X codes
 // and scales (same K, M and output type); the plan is made for the sum of
 // their N, with all_sparse only if every matrix is.
@@ -320,6 +327,7 @@ struct BlockNormParams {
     NormSpec post, pre;
     float scale;
     int C, branch_fp32, residual_fp32, gate_fp32, h_fp32, z_type;
+    int num_sms;
 };
 cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream);
 

@@ -492,55 +492,61 @@ def patch_hybrid_gemm_group(packed: list, X: torch.Tensor, outs: list | None = N
     return outs
 
 
-class _Launch:
-    """The device, stream and row checks shared by the calls below.
+# ---- products with an epilogue, the gated pair, norms.  Every tensor has to be
+# on the current device.  Outputs are allocated for the stream the call runs
+# on, so that the allocator does not hand their memory to other work while the
+# call is still queued.
 
-    Every tensor has to be on the current device.  Outputs are allocated for
-    the stream the call runs on, so that the allocator does not hand their
-    memory to other work while the call is still queued."""
-
-    def __init__(self, x: torch.Tensor, name: str, stream):
-        if not x.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        self.device = x.device
-        if x.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
-        if stream is not None and stream.device != x.device:
-            raise ValueError(f"the stream is on {stream.device}, {name} on {x.device}")
-        self.torch_stream = stream
-        self.stream = _stream(stream)
-
-    def empty(self, shape, dtype) -> torch.Tensor:
-        if self.torch_stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.torch_stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def vector(self, t, n: int, name: str):
-        """Address of an optional contiguous [n] bf16 / fp32 vector."""
-        if t is None:
-            return None
-        if t.device != self.device or t.shape != (n,) or t.dtype not in _REAL or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous bf16 or fp32 vector of {n} on {self.device}")
-        return t.data_ptr()
-
-    def rows(self, t, M: int, C: int, dtypes, name: str) -> tuple:
-        """(address, row stride) of an optional [M, C] tensor whose rows are contiguous."""
-        if t is None:
-            return None, 0
-        if t.device != self.device or t.shape != (M, C) or t.dtype not in dtypes:
-            raise ValueError(f"{name} must be [{M}, {C}] of {dtypes} on {self.device}")
-        step, inner = t.stride()
-        if M <= 1:
-            step = C
-        if (C > 1 and inner != 1) or step < C:
-            raise ValueError(f"{name} must have contiguous rows that do not overlap")
-        return t.data_ptr(), step
+def _launch(x: torch.Tensor, name: str, stream) -> tuple:
+    """(device, raw stream) of a call whose first tensor is x."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    index = dev.index
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(index)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, {name} on {dev}")
+    return dev, stream.cuda_stream
 
 
-def _product_input(packed: list, X: torch.Tensor, x_scales, stream) -> tuple:
-    """Checks of a product's input: (launch, M, address of X, address of the scales)."""
-    at = _Launch(X, "X", stream)
+def _new(like: torch.Tensor, shape: tuple, dtype, stream) -> torch.Tensor:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=like.device)
+    if like.dtype is dtype:
+        return like.new_empty(shape)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _vector(t, n: int, dev, name: str):
+    """Address of an optional contiguous [n] bf16 / fp32 vector."""
+    if t is None:
+        return None
+    if t.device != dev or t.shape != (n,) or t.dtype not in _REAL or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bf16 or fp32 vector of {n} on {dev}")
+    return t.data_ptr()
+
+
+def _rows(t, M: int, C: int, dtypes: tuple, dev, name: str) -> tuple:
+    """(address, row stride) of an optional [M, C] tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if t.device != dev or t.shape != (M, C) or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be [{M}, {C}] of {dtypes} on {dev}")
+    step, inner = t.stride()
+    if M <= 1:
+        step = C
+    if (inner != 1 and C > 1) or step < C:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), step
+
+
+def _product_input(packed, X: torch.Tensor, x_scales, stream) -> tuple:
+    """Checks of a product's input: (device, raw stream, M, address of X, of the scales)."""
+    dev, raw = _launch(X, "X", stream)
     if X.dim() != 2 or not X.is_contiguous():
         raise ValueError("X must be a contiguous [M, K] tensor")
     M, K = X.shape
@@ -548,18 +554,18 @@ def _product_input(packed: list, X: torch.Tensor, x_scales, stream) -> tuple:
         if K != pk.K:
             raise ValueError(f"X has {K} columns, the packed weight {pk.K}")
     if x_scales is None:
-        if X.dtype != torch.bfloat16:
+        if X.dtype is not torch.bfloat16:
             raise ValueError(f"X has dtype {X.dtype}, expected bfloat16 (or e4m3 codes with x_scales)")
-        return at, M, X.data_ptr(), None
+        return dev, raw, M, X.data_ptr(), None
     if X.dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise ValueError(f"X has dtype {X.dtype}, expected e4m3 codes (x_scales is given)")
     for pk in packed:
         if not pk.fp8:
             raise ValueError("x_scales needs FP8 handles (patch_pack_fp8)")
-    if x_scales.device != at.device or x_scales.shape != (M,) or x_scales.dtype != torch.float32 or \
+    if x_scales.device != dev or x_scales.shape != (M,) or x_scales.dtype is not torch.float32 or \
             not x_scales.is_contiguous():
-        raise ValueError(f"x_scales must be a contiguous fp32 vector of {M} on {at.device}")
-    return at, M, X.data_ptr(), x_scales.data_ptr()
+        raise ValueError(f"x_scales must be a contiguous fp32 vector of {M} on {dev}")
+    return dev, raw, M, X.data_ptr(), x_scales.data_ptr()
 
 
 def _activation(name) -> int:
@@ -568,18 +574,19 @@ def _activation(name) -> int:
     return ACTIVATIONS[name]
 
 
-def _epilogue(at: _Launch, pk: PackedWeight, M: int, out, out_fp32: bool, bias, act: int, alpha: float,
-              residual) -> tuple:
-    """(output, PatchEpilogue) of one product, checked."""
+def _output(X: torch.Tensor, M: int, N: int, out, out_fp32: bool, dev, stream) -> tuple:
+    """(output, row stride)."""
     want = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out, y_stride = at.empty((M, pk.N), want), pk.N
-    else:
-        _, y_stride = at.rows(out, M, pk.N, (want,), "out")
-    res, res_stride = at.rows(residual, M, pk.N, _REAL, "residual")
-    return out, PatchEpilogue(at.vector(bias, pk.N, "bias"), res, res_stride, y_stride, alpha, act,
-                              bias is not None and bias.dtype == torch.float32,
-                              residual is not None and residual.dtype == torch.float32)
+        return _new(X, (M, N), want, stream), N
+    return out, _rows(out, M, N, (want,), dev, "out")[1]
+
+
+def _epilogue(M: int, N: int, y_stride: int, bias, act: int, alpha: float, residual, dev) -> PatchEpilogue:
+    r, r_stride = _rows(residual, M, N, _REAL, dev, "residual")
+    return PatchEpilogue(_vector(bias, N, dev, "bias"), r, r_stride, y_stride, alpha, act,
+                         bias is not None and bias.dtype is torch.float32,
+                         r is not None and residual.dtype is torch.float32)
 
 
 def patch_hybrid_linear(packed: PackedWeight, X: torch.Tensor, *, x_scales: torch.Tensor | None = None,
@@ -592,10 +599,13 @@ def patch_hybrid_linear(packed: PackedWeight, X: torch.Tensor, *, x_scales: torc
     handle's input, as patch_quantize_fp8 or patch_block_norm give them.
     activation: "relu", "gelu", "gelu_tanh", "silu" or None.  `out` may be the
     residual itself (in place) and may have rows further apart than N."""
-    at, M, x, xs = _product_input((packed,), X, x_scales, stream)
-    out, epi = _epilogue(at, packed, M, out, out_fp32, bias, _activation(activation), alpha, residual)
-    _check("patch_hybrid_linear", load_library().patch_hybrid_linear(
-        packed.handle, x, xs, M, out.data_ptr(), 1 if out_fp32 else 0, ctypes.byref(epi), at.stream))
+    dev, raw, M, x, xs = _product_input((packed,), X, x_scales, stream)
+    N = packed.N
+    out, y_stride = _output(X, M, N, out, out_fp32, dev, stream)
+    epi = _epilogue(M, N, y_stride, bias, _activation(activation), alpha, residual, dev)
+    code = load_library().patch_hybrid_linear(packed.handle, x, xs, M, out.data_ptr(), 1 if out_fp32 else 0,
+                                              ctypes.byref(epi), raw)
+    _check("patch_hybrid_linear", code)
     return out
 
 
@@ -610,17 +620,18 @@ def patch_hybrid_linear_group(packed: list, X: torch.Tensor, *, x_scales: torch.
     for name, given in (("biases", biases), ("residuals", residuals), ("outs", outs)):
         if given is not None and len(given) != n:
             raise ValueError(f"{name}: one per handle")
-    at, M, x, xs = _product_input(packed, X, x_scales, stream)
+    dev, raw, M, x, xs = _product_input(packed, X, x_scales, stream)
     act = _activation(activation)
     ys, epis = [], (PatchEpilogue * max(n, 1))()
     for i, pk in enumerate(packed):
-        y, epis[i] = _epilogue(at, pk, M, outs[i] if outs else None, out_fp32, biases[i] if biases else None, act,
-                               alpha, residuals[i] if residuals else None)
+        y, y_stride = _output(X, M, pk.N, outs[i] if outs else None, out_fp32, dev, stream)
+        epis[i] = _epilogue(M, pk.N, y_stride, biases[i] if biases else None, act, alpha,
+                            residuals[i] if residuals else None, dev)
         ys.append(y)
     handles = (ctypes.c_void_p * max(n, 1))(*[pk.handle for pk in packed])
     y_p = (ctypes.c_void_p * max(n, 1))(*[y.data_ptr() for y in ys])
-    _check("patch_hybrid_linear_group", load_library().patch_hybrid_linear_group(
-        handles, n, x, xs, M, y_p, 1 if out_fp32 else 0, epis, at.stream))
+    code = load_library().patch_hybrid_linear_group(handles, n, x, xs, M, y_p, 1 if out_fp32 else 0, epis, raw)
+    _check("patch_hybrid_linear_group", code)
     return ys
 
 
@@ -631,36 +642,37 @@ def patch_hybrid_gated(gate: PackedWeight, up: PackedWeight, X: torch.Tensor, *,
     """act(X @ W_gate^T + bias_gate) * (X @ W_up^T + bias_up), rounded once: the
     gated pair of an MLP.  X, x_scales and out as patch_hybrid_linear; the two
     biases share one dtype."""
-    if gate.N != up.N:
-        raise ValueError(f"the gate has {gate.N} rows, the up projection {up.N}")
+    N = gate.N
+    if N != up.N:
+        raise ValueError(f"the gate has {N} rows, the up projection {up.N}")
     if bias_gate is not None and bias_up is not None and bias_gate.dtype != bias_up.dtype:
         raise ValueError("bias_gate and bias_up must have one dtype")
-    at, M, x, xs = _product_input((gate, up), X, x_scales, stream)
-    bg, bu = at.vector(bias_gate, gate.N, "bias_gate"), at.vector(bias_up, gate.N, "bias_up")
+    dev, raw, M, x, xs = _product_input((gate, up), X, x_scales, stream)
+    bg, bu = _vector(bias_gate, N, dev, "bias_gate"), _vector(bias_up, N, dev, "bias_up")
     bias = bias_gate if bias_gate is not None else bias_up
-    want = torch.float32 if out_fp32 else torch.bfloat16
-    if out is None:
-        out, y_stride = at.empty((M, gate.N), want), gate.N
-    else:
-        _, y_stride = at.rows(out, M, gate.N, (want,), "out")
-    _check("patch_hybrid_gated", load_library().patch_hybrid_gated(
+    out, y_stride = _output(X, M, N, out, out_fp32, dev, stream)
+    code = load_library().patch_hybrid_gated(
         gate.handle, up.handle, x, xs, M, out.data_ptr(), y_stride, 1 if out_fp32 else 0, bg, bu,
-        1 if bias is not None and bias.dtype == torch.float32 else 0, _activation(activation), at.stream))
+        1 if bias is not None and bias.dtype is torch.float32 else 0, _activation(activation), raw)
+    _check("patch_hybrid_gated", code)
     return out
 
 
-def _norm(at: _Launch, spec, C: int, name: str) -> PatchNorm:
+_NO_NORM = PatchNorm(0, 0, None, None, 0.0)
+
+
+def _norm(spec, C: int, dev, name: str) -> PatchNorm:
     """(kind, weight, bias, eps) -> PatchNorm; None is no norm."""
     if spec is None:
-        return PatchNorm(0, 0, None, None, 0.0)
+        return _NO_NORM
     kind, weight, bias, eps = spec
     if kind not in NORMS:
         raise ValueError(f"{name} norm {kind!r} is not one of {sorted(NORMS)}")
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise ValueError(f"{name}: weight and bias must have one dtype")
     real = weight if weight is not None else bias
-    return PatchNorm(NORMS[kind], real is not None and real.dtype == torch.float32,
-                     at.vector(weight, C, f"{name} weight"), at.vector(bias, C, f"{name} bias"), eps)
+    return PatchNorm(NORMS[kind], real is not None and real.dtype is torch.float32,
+                     _vector(weight, C, dev, f"{name} weight"), _vector(bias, C, dev, f"{name} bias"), eps)
 
 
 def patch_block_norm(branch: torch.Tensor, *, residual: torch.Tensor | None = None,
@@ -676,45 +688,49 @@ def patch_block_norm(branch: torch.Tensor, *, residual: torch.Tensor | None = No
     row).  post and pre are (kind, weight, bias, eps) with kind "rms" or
     "layer" and weight, bias [C] or None; post None means no norm.  z is given
     where there is a `pre` or z_type is "e4m3" (codes and a scale per token for
-    patch_hybrid_linear's x_scales).  out_h may be the residual or the branch,
-    out_z the branch (in place).  Returns {"h", "z", "scales"}."""
-    at = _Launch(branch, "branch", stream)
+    patch_hybrid_linear's x_scales).  out_h and out_z may each be the residual
+    or the branch (in place), not both the same.  Returns {"h", "z", "scales"}."""
+    dev, raw = _launch(branch, "branch", stream)
     if branch.dim() != 2:
         raise ValueError("branch must be [M, C]")
     M, C = branch.shape
     if z_type not in Z_TYPES:
         raise ValueError(f"z_type {z_type!r} is not one of {sorted(Z_TYPES)}")
-    b, b_step = at.rows(branch, M, C, _REAL, "branch")
-    r, r_step = at.rows(residual, M, C, _REAL, "residual")
+    b, b_step = _rows(branch, M, C, _REAL, dev, "branch")
+    r, r_step = _rows(residual, M, C, _REAL, dev, "residual")
     g, g_step, g_tokens = None, 0, 1
     if gate is not None:
         rows = 1 if gate.dim() == 1 else gate.shape[0]
         if rows < 1 or M % rows:
             raise ValueError(f"gate has {rows} rows, which do not divide {M} tokens")
-        g, g_step = at.rows(gate if gate.dim() == 2 else gate.view(1, -1), rows, C, _REAL, "gate")
+        g, g_step = _rows(gate if gate.dim() == 2 else gate.view(1, -1), rows, C, _REAL, dev, "gate")
         g_tokens = max(M // rows, 1)
     h_type = torch.float32 if h_fp32 else torch.bfloat16
     if out_h is None:
-        out_h = at.empty((M, C), h_type)
-    h, h_step = at.rows(out_h, M, C, (h_type,), "out_h")
-    z = scales = None
+        out_h, h_step = _new(branch, (M, C), h_type, stream), C
+        h = out_h.data_ptr()
+    else:
+        h, h_step = _rows(out_h, M, C, (h_type,), dev, "out_h")
+    z = scales = s = None
     z_step = 0
     want = Z_TYPES[z_type] if pre is not None or z_type == "e4m3" else 0
     if want:
         z_dtype = (torch.bfloat16, torch.float32, torch.uint8)[want - 1]
         if out_z is None:
-            out_z = at.empty((M, C), z_dtype)
-        z, z_step = at.rows(out_z, M, C, (z_dtype,), "out_z")
+            out_z, z_step = _new(branch, (M, C), z_dtype, stream), C
+            z = out_z.data_ptr()
+        else:
+            z, z_step = _rows(out_z, M, C, (z_dtype,), dev, "out_z")
         if want == 3:
-            scales = at.empty((M,), torch.float32)
+            scales = _new(branch, (M,), torch.float32, stream)
+            s = scales.data_ptr()
     elif out_z is not None:
         raise ValueError("out_z without a pre norm")
-    args = PatchBlockNormArgs(b, b_step, r, r_step, g, g_step, g_tokens, h, h_step, z, z_step,
-                              scales.data_ptr() if scales is not None else None, _norm(at, post, C, "post"),
-                              _norm(at, pre, C, "pre"), scale, branch.dtype == torch.float32,
-                              residual is not None and residual.dtype == torch.float32,
-                              gate is not None and gate.dtype == torch.float32, h_fp32, want)
-    _check("patch_block_norm", load_library().patch_block_norm(ctypes.byref(args), M, C, at.stream))
+    args = PatchBlockNormArgs(b, b_step, r, r_step, g, g_step, g_tokens, h, h_step, z, z_step, s,
+                              _norm(post, C, dev, "post"), _norm(pre, C, dev, "pre"), scale,
+                              branch.dtype is torch.float32, r is not None and residual.dtype is torch.float32,
+                              g is not None and gate.dtype is torch.float32, h_fp32, want)
+    _check("patch_block_norm", load_library().patch_block_norm(ctypes.byref(args), M, C, raw))
     return {"h": out_h, "z": out_z if want else None, "scales": scales}
 
 
