@@ -524,7 +524,9 @@ patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const fl
  * counts, one two-SM launch in prefill, one quantisation of X).
  *   epis   host array of count epilogues, or NULL for none.
  * Every member's arguments are checked before anything is enqueued.  A
- * handle may appear more than once.  The outputs must not overlap one another.
+ * handle may appear more than once.  The members run in no order: an output
+ * must overlap no other output and no other member's residual (INVALID_ARG
+ * where one starts at the address of another).
  */
 patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t count, const void *X,
                                        const float *x_scales, int64_t M, void *const *Ys,

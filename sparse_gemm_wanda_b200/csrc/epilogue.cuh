@@ -21,10 +21,16 @@ enum EpiMode { kEpiPlain = 0, kEpiLinear = 1, kEpiGated = 2 };
 // The activations, through CUDA's own math functions.
 __device__ __forceinline__ float act_relu(float v) { return v < 0.0f ? 0.0f : v; }  // NaN stays NaN
 __device__ __forceinline__ float act_gelu(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678f)); }
+// x / (1 + exp(-y)) by the hardware's exponential and reciprocal: off by at most
+// about 2^-21 + 2^-24 |y| of the result, against 2^-9 for a bf16 output.  Eight
+// warps finish an accumulator, so a short K is bound by these instructions
+// (FP8, 2478 tokens, 7168x256 gated: 77 us with tanhf).
+__device__ __forceinline__ float over_one_plus_exp(float x, float y) { return __fdividef(x, 1.0f + __expf(-y)); }
+// (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u))
 __device__ __forceinline__ float act_gelu_tanh(float v) {
-    return 0.5f * v * (1.0f + tanhf(0.79788456f * (v + 0.044715f * v * v * v)));
+    return over_one_plus_exp(v, v * fmaf(0.07135481f * v, v, 1.59576912f));
 }
-__device__ __forceinline__ float act_silu(float v) { return v / (1.0f + expf(-v)); }
+__device__ __forceinline__ float act_silu(float v) { return over_one_plus_exp(v, v); }
 
 // `act` is the same for the whole launch: one uniform branch per NV values.
 template <int NV>
@@ -117,6 +123,25 @@ __device__ __forceinline__ void epi_store(const Epilogue &e, void *Y, int y_fp32
         v[q] = e.mul ? v[q] * a : fmaf(e.alpha, v[q], a);
     }
     store_column(Y, m0 * e.ldy + n, e.ldy, count, v, y_fp32);
+}
+
+// The chunks c, c + step, ... of an accumulator finished and stored; `sums(c, v)`
+// reads 16 sums, `add` holds what epi_fetch gave for the first chunk.  The next
+// chunk's residual is on its way while a chunk is stored.
+template <class Sums>
+__device__ __forceinline__ void epi_drain(const Epilogue &e, void *Y, int y_fp32, int64_t N, int c, int step,
+                                          int64_t m_base, int m_valid, int64_t n, float bias, uint32_t (&add)[16],
+                                          const Sums &sums) {
+#pragma unroll 1
+    for (; c < m_valid; c += step) {
+        float v[16];
+        uint32_t next[16];
+        sums(c, v);
+        epi_fetch(e, N, m_base + c + step, n, m_valid - c - step, next);
+        epi_store(e, Y, y_fp32, m_base + c, n, m_valid - c, bias, v, add);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) add[q] = next[q];
+    }
 }
 
 // One piece of a gated item in a two-SM kernel: this thread's output column n

@@ -300,25 +300,26 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     for (int q = 0; q < 16; ++q)
                         if (c0 + q < m_valid) part[(c0 + q) * kBand] = __uint_as_float(r[q]);
                 }
-            } else if (*abort_flag == 0) {
-                [[maybe_unused]] float bias = 0.0f;
-                if constexpr (EPI) bias = epi_bias(p.epi, n);
+            } else if (*abort_flag != 0) {
+            } else if constexpr (EPI) {
+                uint32_t add[16];
+                epi_fetch(p.epi, p.N, m_base, n, m_valid, add);
+                auto scaled = [&](int c0, float(&v)[16]) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
+                    // token scales of the chunk: lane l holds column l % 16's
+                    const int ml = c0 + (lane & 15);
+                    const float sxl = ml < m_valid ? __ldg(p.sx + m_base + ml) : 0.0f;
+                    tmem_ld_wait(r);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        v[q] = __uint_as_float(r[q]) * swn * __shfl_sync(0xFFFFFFFFu, sxl, q);
+                };
+                epi_drain(p.epi, p.Y, p.y_fp32, p.N, 0, 16, m_base, m_valid, n, epi_bias(p.epi, n), add, scaled);
+            } else {
 #pragma unroll 1
                 for (int c0 = 0; c0 < m_valid; c0 += 16) {
                     uint32_t r[16];
-                    if constexpr (EPI) {
-                        uint32_t add[16];
-                        float v[16];
-                        epi_fetch(p.epi, p.N, m_base + c0, n, m_valid - c0, add);
-                        tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
-                        tmem_ld_wait(r);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            v[q] = c0 + q < m_valid
-                                       ? __uint_as_float(r[q]) * swn * __ldg(p.sx + m_base + c0 + q) : 0.0f;
-                        epi_store(p.epi, p.Y, p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
-                        continue;
-                    }
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
                     tmem_ld_wait();
 #pragma unroll

@@ -543,15 +543,24 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             const int m_valid = static_cast<int>(min(static_cast<int64_t>(BN), p.M - m_base));
             float *part = (sg.nsegs > 1) ? p.partial + static_cast<int64_t>(sg.slot) * BN * kBand
                                          : nullptr;
-            [[maybe_unused]] float bias = 0.0f;
-            if constexpr (EPI) bias = epi_bias(p.epi, n);
-#pragma unroll 1
-            for (int c0 = 0; c0 < BN; c0 += 16) {
-                uint32_t r[16];
-                [[maybe_unused]] uint32_t add[16];
-                if constexpr (EPI) {
-                    if (!part && live) epi_fetch(p.epi, p.N, m_base + c0, n, m_valid - c0, add);
+            const bool whole = EPI && !part;  // this CTA's sums are the product's
+            if constexpr (EPI) {
+                if (whole && live) {
+                    uint32_t add[16];
+                    epi_fetch(p.epi, p.N, m_base, n, m_valid, add);
+                    auto sums = [&](int c0, float(&v)[16]) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(lane_base + buf * BN + c0, r);
+                        tmem_ld_wait(r);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
+                    };
+                    epi_drain(p.epi, p.Y, p.y_fp32, p.N, 0, 16, m_base, m_valid, n, epi_bias(p.epi, n), add, sums);
                 }
+            }
+#pragma unroll 1
+            for (int c0 = 0; c0 < (whole ? 0 : BN); c0 += 16) {
+                uint32_t r[16];
                 tmem_ld_32x32b_x16(lane_base + buf * BN + c0, r);
                 tmem_ld_wait();
                 if (!live) continue;
@@ -559,11 +568,6 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         if (c0 + q < m_valid) part[(c0 + q) * kBand + row] = __uint_as_float(r[q]);
-                } else if constexpr (EPI) {
-                    float v[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
-                    epi_store(p.epi, p.Y, p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
                 } else {
 #pragma unroll
                     for (int q = 0; q < 16; ++q)

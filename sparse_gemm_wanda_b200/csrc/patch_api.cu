@@ -161,6 +161,17 @@ patch_status from_cuda(cudaError_t e) {
     return PATCH_ERR_CUDA;
 }
 
+// Host-side planning allocates; running out of host memory is an error of the
+// call, not an exception through the C boundary.
+template <class Call>
+patch_status no_throw(const Call &call) {
+    try {
+        return call();
+    } catch (...) {
+        return PATCH_ERR_OOM;
+    }
+}
+
 // epi null: the plain product
 template <class Launch>
 void set_epilogue(Launch &g, const patchk::Epilogue *epi) {
@@ -1127,12 +1138,22 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
     for (int i = 0; i < count && one_launch; ++i)
         one_launch = Wps[i]->pattern == 2 && Wps[i]->shp.K == K && Wps[i]->num_sms == Wps[0]->num_sms;
     if (!one_launch) {
-        // the products one after another on the stream (the same results)
-        for (int i = 0; i < count; ++i) {
-            const patch_status st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream);
-            if (st != PATCH_OK) return st;
+        // the products one after another on the stream (the same results);
+        // FP8 handles with epilogues share one quantisation of X
+        XCodes x;
+        bool share = epis && count > 1 && !x_scales;
+        for (int i = 0; i < count && share; ++i) share = Wps[i]->pattern == 8;
+        if (share) {
+            const cudaError_t e = codes_of(Wps[0], X, x_scales, M, &x, stream);
+            if (e != cudaSuccess) return free_codes(x, e, stream);
+            X = x.q;
+            x_scales = x.s;
         }
-        return PATCH_OK;
+        patch_status st = PATCH_OK;
+        for (int i = 0; i < count && st == PATCH_OK; ++i)
+            st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream);
+        const patch_status st2 = free_codes(x, cudaSuccess, stream);
+        return st != PATCH_OK ? st : st2;
     }
     patchk::GemmLaunch gs[patchk::kDecMaxGroup];
     for (int i = 0; i < count; ++i) gs[i] = gemm_launch(Wps[i], X, M, Ys[i], y_is_fp32, epi(i));
@@ -1263,9 +1284,14 @@ patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t c
         st = check_epilogue(epis ? epis + i : nullptr, Wps[i]->shp.N, M, Ys[i], y_is_fp32, &es[i]);
         if (st != PATCH_OK) return st;
     }
+    // the members run in no order: none may write what another writes or reads
+    for (int i = 0; i < count && M > 0; ++i)
+        for (int j = 0; j < count; ++j)
+            if (i != j && (Ys[i] == Ys[j] || Ys[i] == es[j].residual)) return PATCH_ERR_INVALID_ARG;
     if (M == 0) return PATCH_OK;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-    return products(Wps, count, X, x_scales, M, Ys, y_is_fp32, es, stream);
+    return no_throw([&] {
+        return products(Wps, count, X, x_scales, M, Ys, y_is_fp32, es, static_cast<cudaStream_t>(stream_v));
+    });
 }
 
 patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
@@ -1291,8 +1317,9 @@ patch_status patch_hybrid_gated(const patch_packed *Wgate, const patch_packed *W
     up.bias = bias_up;
     up.bias_fp32 = bias_is_fp32;
     up.ldy = e.ldy;
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-    return gated_products(hs, X, x_scales, M, Y, y_is_fp32, e, up, stream);
+    return no_throw([&] {
+        return gated_products(hs, X, x_scales, M, Y, y_is_fp32, e, up, static_cast<cudaStream_t>(stream_v));
+    });
 }
 
 // ------------------------------------------------------- norms of a block

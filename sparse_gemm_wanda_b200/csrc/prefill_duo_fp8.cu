@@ -438,17 +438,7 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
             };
             if (*abort_flag != 0) {
             } else if constexpr (MODE == kEpiLinear) {
-#pragma unroll 1
-                for (int c0 = 16 * grp; c0 < m_valid; c0 += 32) {
-                    float v[16];
-                    uint32_t next[16];
-                    scaled(c0, v);
-                    // the next chunk's residual is on its way while this one is stored
-                    epi_fetch(p.epi[mi], p.N[mi], m_base + c0 + 32, n, m_valid - c0 - 32, next);
-                    epi_store(p.epi[mi], p.Y[mi], p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) add[q] = next[q];
-                }
+                epi_drain(p.epi[mi], p.Y[mi], p.y_fp32, p.N[mi], 16 * grp, 32, m_base, m_valid, n, bias, add, scaled);
             } else if constexpr (MODE == kEpiGated) {
                 gated_piece(p.epi[mi], p.Y[0], p.y_fp32, mi, lane_base + static_cast<uint32_t>(buf * bn), grp,
                             m_base, m_valid, n, bias, held, scaled);

@@ -351,19 +351,16 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
             const int m_valid = static_cast<int>(min(static_cast<int64_t>(bn), p.M - m_base));
             if constexpr (EPI) {
                 if (live) {
-                    const float bias = epi_bias(p.epi, n);
-#pragma unroll 1
-                    for (int c0 = 0; c0 < m_valid; c0 += 16) {
+                    uint32_t add[16];
+                    epi_fetch(p.epi, p.N, m_base, n, m_valid, add);
+                    auto sums = [&](int c0, float(&v)[16]) {
                         uint32_t r[16];
-                        uint32_t add[16];
-                        float v[16];
-                        epi_fetch(p.epi, p.N, m_base + c0, n, m_valid - c0, add);
                         tmem_ld_32x32b_x16(lane_base + c0, r);
                         tmem_ld_wait(r);
 #pragma unroll
                         for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
-                        epi_store(p.epi, p.Y, p.y_fp32, m_base + c0, n, m_valid - c0, bias, v, add);
-                    }
+                    };
+                    epi_drain(p.epi, p.Y, p.y_fp32, p.N, 0, 16, m_base, m_valid, n, epi_bias(p.epi, n), add, sums);
                 }
             } else if (live) {
 #pragma unroll 1

@@ -500,10 +500,10 @@ def patch_hybrid_gemm_group(packed: list, X: torch.Tensor, outs: list | None = N
 def _launch(x: torch.Tensor, name: str, stream) -> tuple:
     """(device, raw stream) of a call whose first tensor is x."""
     dev = x.device
-    if dev.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     index = dev.index
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(index)
@@ -516,6 +516,8 @@ def _new(like: torch.Tensor, shape: tuple, dtype, stream) -> torch.Tensor:
     if stream is not None:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=like.device)
+    if like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like) if like.dtype is dtype else torch.empty_like(like, dtype=dtype)
     if like.dtype is dtype:
         return like.new_empty(shape)
     return torch.empty(shape, dtype=dtype, device=like.device)
@@ -525,7 +527,7 @@ def _vector(t, n: int, dev, name: str):
     """Address of an optional contiguous [n] bf16 / fp32 vector."""
     if t is None:
         return None
-    if t.device != dev or t.shape != (n,) or t.dtype not in _REAL or not t.is_contiguous():
+    if t.device != dev or t.dtype not in _REAL or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bf16 or fp32 vector of {n} on {dev}")
     return t.data_ptr()
 
@@ -583,10 +585,14 @@ def _output(X: torch.Tensor, M: int, N: int, out, out_fp32: bool, dev, stream) -
 
 
 def _epilogue(M: int, N: int, y_stride: int, bias, act: int, alpha: float, residual, dev) -> PatchEpilogue:
+    if residual is None:
+        if bias is None:
+            return PatchEpilogue(None, None, 0, y_stride, alpha, act)
+        return PatchEpilogue(_vector(bias, N, dev, "bias"), None, 0, y_stride, alpha, act,
+                             bias.dtype is torch.float32)
     r, r_stride = _rows(residual, M, N, _REAL, dev, "residual")
     return PatchEpilogue(_vector(bias, N, dev, "bias"), r, r_stride, y_stride, alpha, act,
-                         bias is not None and bias.dtype is torch.float32,
-                         r is not None and residual.dtype is torch.float32)
+                         bias is not None and bias.dtype is torch.float32, residual.dtype is torch.float32)
 
 
 def patch_hybrid_linear(packed: PackedWeight, X: torch.Tensor, *, x_scales: torch.Tensor | None = None,

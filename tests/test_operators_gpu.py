@@ -224,8 +224,9 @@ def test_group(P, gen, kinds, M):
         check_linear(y, w, x, xs, b, "gelu_tanh", -2.0, r)
 
 
-def test_the_same_handle_twice(P, gen):
-    w = Weight(P, gen, 256, 512)
+@pytest.mark.parametrize("kind", ["2:4", "fp8", "4:8"])
+def test_the_same_handle_twice(P, gen, kind):
+    w = Weight(P, gen, 256, 512, kind)
     for M in (4, 40, 300):
         x, _ = x_of(gen, w, M)
         b = randn(gen, 256)
@@ -316,6 +317,12 @@ def test_refusals(P, gen):
     wide = torch.zeros(8, 512, dtype=BF, device="cuda")
     with pytest.raises(P.PatchError):
         P.patch_hybrid_linear(w.packed, x, residual=wide[:4, :256], out=wide.view(-1)[:1024].view(4, 256))
+    # members of a group that write what another writes or reads
+    r = torch.zeros(4, 256, dtype=BF, device="cuda")
+    with pytest.raises(P.PatchError):
+        P.patch_hybrid_linear_group([w.packed, w.packed], x, outs=[r, r])
+    with pytest.raises(P.PatchError):
+        P.patch_hybrid_linear_group([w.packed, w.packed], x, outs=[r, None], residuals=[r, r])
     # through the C ABI: bad flags, strides and alignment are errors, nothing runs
     lib, y = P.load_library(), torch.full((4, 256), 7.0, dtype=BF, device="cuda")
 
@@ -602,3 +609,49 @@ def test_norm_codes_are_the_rounded_quotients(P, gen, spread):
             assert torch.equal(codes["scales"], s)
             assert torch.equal(codes["z"], q.view(torch.uint8))
         assert z.shape == e["z"].shape
+
+
+def test_first_call_inside_a_capture():
+    # a program whose first norm of a kind runs inside a stream capture
+    import subprocess
+    import sys
+    code = """
+import torch
+from sparse_gemm_wanda_b200 import patch as P
+x = torch.randn(64, 4096, device="cuda").bfloat16()
+big = torch.randn(4096, 4096, device="cuda").bfloat16()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    z = P.patch_block_norm(x, pre=("rms", None, None, 1e-5))["z"]
+    y = P.patch_block_norm(big, residual=big, pre=("rms", None, None, 1e-5))["z"]
+graph.replay()
+torch.cuda.synchronize()
+for got, row in ((z, x.double()), (y, 2 * big.double())):
+    want = row / (row.pow(2).mean(1, keepdim=True) + 1e-5).sqrt()
+    assert ((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all()
+print("replayed")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M,C", [(4096, 4096), (3001, 5120), (1500, 8192), (900, 16384), (20000, 1024)])
+def test_norm_many_rows(P, gen, M, C):
+    # the sizes that run through the shared-memory ring, with every part of it present and absent
+    bf = dict(dtype=BF)
+    b, r = randn(gen, M, C, **bf), randn(gen, M, C, **bf)
+    rms = lambda: ("rms", randn(gen, C, spread=0.2, **bf) + 1, None, 1e-5)  # noqa: E731
+    check_norm(P, b, r, pre=rms())
+    check_norm(P, b, None, pre=("rms", None, None, 1e-5), scale=0.5)
+    check_norm(P, b, r, gate=randn(gen, C, **bf), scale=-0.5, post=rms(), pre=rms())
+    check_norm(P, b, r, gate=randn(gen, 1, C), post=("rms", None, None, 1e-5), pre=None)
+    check_norm(P, b, r, post=("rms", randn(gen, C), None, 1e-5), pre=("rms", randn(gen, C), None, 1e-5), z_type="e4m3")
+    # rows further apart than C, in place
+    wide_b, wide_r = randn(gen, M, C + 8, **bf), randn(gen, M, C + 16, **bf)
+    want = P.patch_block_norm(wide_b[:, :C].contiguous(), residual=wide_r[:, :C].contiguous(), pre=rms())
+    keep = wide_r[:, C:].clone()
+    got = P.patch_block_norm(wide_b[:, :C], residual=wide_r[:, :C], out_h=wide_r[:, :C])
+    assert torch.equal(got["h"], want["h"]) and torch.equal(wide_r[:, C:], keep)
