@@ -2,7 +2,9 @@
 
 ``python -m sparse_gemm_wanda_b200.build`` (or ``build()``) compiles every
 ``csrc/*.cu`` with nvcc for ``compute_100a``/``sm_100a`` and links one shared
-library next to this file.  nvcc cross-compiles, so no GPU is needed to build.
+library next to this file, and ``csrc/torch_binding.cpp`` with g++ against the
+installed PyTorch into ``_patch_torch.so`` beside it.  nvcc cross-compiles, so
+no GPU is needed to build.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libpatch_b200.so")
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING_OUT = os.path.join(HERE, "_patch_torch.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -41,7 +45,38 @@ def _stale(srcs, out) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_binding() -> None:
+    """The CPython module over PyTorch tensors (csrc/torch_binding.cpp)."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    lib = os.path.join(base, "lib")
+    tmp = BINDING_OUT + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_path("include"), "-I", INCLUDE, *[f"-isystem{p}" for p in include], BINDING_SRC,
+           "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_OUT)
+
+
+def _stale_binding() -> bool:
+    if not os.path.exists(BINDING_OUT):
+        return True
+    t = os.path.getmtime(BINDING_OUT)
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "patch.h"), os.path.abspath(__file__)]
+    return any(os.path.getmtime(d) > t for d in deps)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    if force or _stale_binding():
+        _build_binding()
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     if not force and not _stale(srcs, OUT):
         return OUT

@@ -754,16 +754,16 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, 
     if (nchunks > kDecMaxChunksPerCta) return cudaErrorInvalidValue;
     p.nchunks = static_cast<int>(nchunks);
     const int grid = static_cast<int>(std::min<int64_t>(std::min<int64_t>(g.num_sms, nchunks), kDecMaxCtas));
-    // host copy of chunk c's descriptor
-    auto desc_of = [&](int64_t c) {
-        int i = 0;
-        while (i + 1 < count && p.band0[i + 1] * static_cast<int64_t>(g.dec_cpb) <= c) ++i;
-        return gs[i].chunk_desc_host[c - static_cast<int64_t>(p.band0[i]) * g.dec_cpb];
+    // the descriptors of chunks c and c + grid, from the matrices' host copies
+    auto copy_desc = [&](uint64_t *dst, int64_t c0, int64_t c1) {
+        for (int i = 0; i < count; ++i) {
+            const int64_t base = static_cast<int64_t>(p.band0[i]) * g.dec_cpb;
+            const int64_t a = std::max(c0, base), b = std::min(c1, base + gs[i].dec_nchunks);
+            if (a < b) std::copy(gs[i].chunk_desc_host + (a - base), gs[i].chunk_desc_host + (b - base), dst + (a - c0));
+        }
     };
-    for (int c = 0; c < kDecMaxCtas; ++c) {
-        p.first_desc[c] = c < grid ? desc_of(c) : 0ull;
-        p.second_desc[c] = (c < grid && c + grid < nchunks) ? desc_of(c + grid) : 0ull;
-    }
+    copy_desc(p.first_desc, 0, grid);
+    copy_desc(p.second_desc, grid, std::min<int64_t>(nchunks, 2 * grid));
     // partials: each handle's own slots (16 token rows per chunk) where they
     // are large enough; otherwise one block from the stream-ordered pool for
     // the call, cut per matrix

@@ -8,6 +8,7 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -31,12 +32,10 @@ EXPORTS = ("patch_score_mask", "patch_pack", "patch_hybrid_gemm", "patch_free",
            "patch_hybrid_linear", "patch_hybrid_linear_group", "patch_hybrid_gated",
            "patch_block_norm")
 
-# patch_activation, patch_norm_kind and patch_z_type of include/patch.h
+# patch_activation and patch_z_type of include/patch.h
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
-NORMS = {"rms": 1, "layer": 2}
 Z_TYPES = {"bf16": 1, "fp32": 2, "e4m3": 3}
 NORM_MAX_C = 32768
-_REAL = (torch.bfloat16, torch.float32)
 
 
 class PatchLibraryError(RuntimeError):
@@ -332,6 +331,7 @@ class PackedWeight:
         self.N, self.K, self.tile_n, self.tile_k = shape
         self.packed_bytes = packed_bytes
         self.fp8 = fp8
+        self._info = (int(handle or 0), self.N, self.K, fp8)  # as the native marshalling takes it
 
     def view(self) -> PatchPackedView:
         v = PatchPackedView()
@@ -359,6 +359,7 @@ class PackedWeight:
         if self.handle and self.handle.value:
             load_library().patch_free(self.handle, _stream(stream))
             self.handle = ctypes.c_void_p(0)
+            self._info = (0,) + self._info[1:]
 
     def __del__(self):
         try:
@@ -492,107 +493,54 @@ def patch_hybrid_gemm_group(packed: list, X: torch.Tensor, outs: list | None = N
     return outs
 
 
-# ---- products with an epilogue, the gated pair, norms.  Every tensor has to be
-# on the current device.  Outputs are allocated for the stream the call runs
-# on, so that the allocator does not hand their memory to other work while the
-# call is still queued.
+# ---- products with an epilogue, the gated pair, norms: marshalled by the
+# native module of csrc/torch_binding.cpp (checks, output allocation, the call
+# into the C ABI).  Every tensor has to be on the current device; work and new
+# outputs belong to the current stream, or to the one given.
 
-def _launch(x: torch.Tensor, name: str, stream) -> tuple:
-    """(device, raw stream) of a call whose first tensor is x."""
-    dev = x.device
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    index = dev.index
-    if index != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+_native = None
+
+
+def _load_native():
+    global _native
+    if _native is None:
+        lib = load_library()
+        path = os.path.join(_HERE, "_patch_torch.so")
+        if not os.path.exists(path):
+            raise PatchLibraryError(
+                f"{path} is missing: build it with `python -m sparse_gemm_wanda_b200.build`")
+        spec = importlib.util.spec_from_file_location("_patch_torch", path)
+        try:
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+        except ImportError as exc:
+            raise PatchLibraryError(f"cannot load {path}: {exc}") from exc
+        module.bind(*[ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (lib.patch_hybrid_linear_group, lib.patch_hybrid_gated, lib.patch_block_norm)])
+        _native = module
+    return _native
+
+
+def _run(fn: str, name: str, stream, *args):
+    """The native call on the current stream, or on `stream`; a status is raised as PatchError."""
+    call = getattr(_native or _load_native(), name)
     if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(index)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, {name} on {dev}")
-    return dev, stream.cuda_stream
-
-
-def _new(like: torch.Tensor, shape: tuple, dtype, stream) -> torch.Tensor:
-    if stream is not None:
+        r = call(*args)
+    else:
+        if stream.device.index != torch.cuda.current_device():
+            raise ValueError(f"the stream is on {stream.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=like.device)
-    if like.shape == shape and like.is_contiguous():
-        return torch.empty_like(like) if like.dtype is dtype else torch.empty_like(like, dtype=dtype)
-    if like.dtype is dtype:
-        return like.new_empty(shape)
-    return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _vector(t, n: int, dev, name: str):
-    """Address of an optional contiguous [n] bf16 / fp32 vector."""
-    if t is None:
-        return None
-    if t.device != dev or t.dtype not in _REAL or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous bf16 or fp32 vector of {n} on {dev}")
-    return t.data_ptr()
-
-
-def _rows(t, M: int, C: int, dtypes: tuple, dev, name: str) -> tuple:
-    """(address, row stride) of an optional [M, C] tensor whose rows are contiguous."""
-    if t is None:
-        return None, 0
-    if t.device != dev or t.shape != (M, C) or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be [{M}, {C}] of {dtypes} on {dev}")
-    step, inner = t.stride()
-    if M <= 1:
-        step = C
-    if (inner != 1 and C > 1) or step < C:
-        raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.data_ptr(), step
-
-
-def _product_input(packed, X: torch.Tensor, x_scales, stream) -> tuple:
-    """Checks of a product's input: (device, raw stream, M, address of X, of the scales)."""
-    dev, raw = _launch(X, "X", stream)
-    if X.dim() != 2 or not X.is_contiguous():
-        raise ValueError("X must be a contiguous [M, K] tensor")
-    M, K = X.shape
-    for pk in packed:
-        if K != pk.K:
-            raise ValueError(f"X has {K} columns, the packed weight {pk.K}")
-    if x_scales is None:
-        if X.dtype is not torch.bfloat16:
-            raise ValueError(f"X has dtype {X.dtype}, expected bfloat16 (or e4m3 codes with x_scales)")
-        return dev, raw, M, X.data_ptr(), None
-    if X.dtype not in (torch.uint8, torch.float8_e4m3fn):
-        raise ValueError(f"X has dtype {X.dtype}, expected e4m3 codes (x_scales is given)")
-    for pk in packed:
-        if not pk.fp8:
-            raise ValueError("x_scales needs FP8 handles (patch_pack_fp8)")
-    if x_scales.device != dev or x_scales.shape != (M,) or x_scales.dtype is not torch.float32 or \
-            not x_scales.is_contiguous():
-        raise ValueError(f"x_scales must be a contiguous fp32 vector of {M} on {dev}")
-    return dev, raw, M, X.data_ptr(), x_scales.data_ptr()
+            r = call(*args)
+    if type(r) is int:
+        raise PatchError(fn, r)
+    return r
 
 
 def _activation(name) -> int:
     if name not in ACTIVATIONS:
         raise ValueError(f"activation {name!r} is not one of {sorted(k for k in ACTIVATIONS if k)}")
     return ACTIVATIONS[name]
-
-
-def _output(X: torch.Tensor, M: int, N: int, out, out_fp32: bool, dev, stream) -> tuple:
-    """(output, row stride)."""
-    want = torch.float32 if out_fp32 else torch.bfloat16
-    if out is None:
-        return _new(X, (M, N), want, stream), N
-    return out, _rows(out, M, N, (want,), dev, "out")[1]
-
-
-def _epilogue(M: int, N: int, y_stride: int, bias, act: int, alpha: float, residual, dev) -> PatchEpilogue:
-    if residual is None:
-        if bias is None:
-            return PatchEpilogue(None, None, 0, y_stride, alpha, act)
-        return PatchEpilogue(_vector(bias, N, dev, "bias"), None, 0, y_stride, alpha, act,
-                             bias.dtype is torch.float32)
-    r, r_stride = _rows(residual, M, N, _REAL, dev, "residual")
-    return PatchEpilogue(_vector(bias, N, dev, "bias"), r, r_stride, y_stride, alpha, act,
-                         bias is not None and bias.dtype is torch.float32, residual.dtype is torch.float32)
 
 
 def patch_hybrid_linear(packed: PackedWeight, X: torch.Tensor, *, x_scales: torch.Tensor | None = None,
@@ -605,14 +553,8 @@ def patch_hybrid_linear(packed: PackedWeight, X: torch.Tensor, *, x_scales: torc
     handle's input, as patch_quantize_fp8 or patch_block_norm give them.
     activation: "relu", "gelu", "gelu_tanh", "silu" or None.  `out` may be the
     residual itself (in place) and may have rows further apart than N."""
-    dev, raw, M, x, xs = _product_input((packed,), X, x_scales, stream)
-    N = packed.N
-    out, y_stride = _output(X, M, N, out, out_fp32, dev, stream)
-    epi = _epilogue(M, N, y_stride, bias, _activation(activation), alpha, residual, dev)
-    code = load_library().patch_hybrid_linear(packed.handle, x, xs, M, out.data_ptr(), 1 if out_fp32 else 0,
-                                              ctypes.byref(epi), raw)
-    _check("patch_hybrid_linear", code)
-    return out
+    return _run("patch_hybrid_linear", "linear", stream, (packed._info,), X, x_scales, (bias,),
+                _activation(activation), alpha, (residual,), (out,), out_fp32)[0]
 
 
 def patch_hybrid_linear_group(packed: list, X: torch.Tensor, *, x_scales: torch.Tensor | None = None,
@@ -622,23 +564,8 @@ def patch_hybrid_linear_group(packed: list, X: torch.Tensor, *, x_scales: torch.
     """patch_hybrid_linear for 1 to 8 handles that read the same X, launched
     together where the library can; one bias / residual / output (or None) per
     handle, one activation and alpha for all."""
-    n = len(packed)
-    for name, given in (("biases", biases), ("residuals", residuals), ("outs", outs)):
-        if given is not None and len(given) != n:
-            raise ValueError(f"{name}: one per handle")
-    dev, raw, M, x, xs = _product_input(packed, X, x_scales, stream)
-    act = _activation(activation)
-    ys, epis = [], (PatchEpilogue * max(n, 1))()
-    for i, pk in enumerate(packed):
-        y, y_stride = _output(X, M, pk.N, outs[i] if outs else None, out_fp32, dev, stream)
-        epis[i] = _epilogue(M, pk.N, y_stride, biases[i] if biases else None, act, alpha,
-                            residuals[i] if residuals else None, dev)
-        ys.append(y)
-    handles = (ctypes.c_void_p * max(n, 1))(*[pk.handle for pk in packed])
-    y_p = (ctypes.c_void_p * max(n, 1))(*[y.data_ptr() for y in ys])
-    code = load_library().patch_hybrid_linear_group(handles, n, x, xs, M, y_p, 1 if out_fp32 else 0, epis, raw)
-    _check("patch_hybrid_linear_group", code)
-    return ys
+    return _run("patch_hybrid_linear_group", "linear", stream, [p._info for p in packed], X, x_scales, biases,
+                _activation(activation), alpha, residuals, outs, out_fp32)
 
 
 def patch_hybrid_gated(gate: PackedWeight, up: PackedWeight, X: torch.Tensor, *,
@@ -648,37 +575,8 @@ def patch_hybrid_gated(gate: PackedWeight, up: PackedWeight, X: torch.Tensor, *,
     """act(X @ W_gate^T + bias_gate) * (X @ W_up^T + bias_up), rounded once: the
     gated pair of an MLP.  X, x_scales and out as patch_hybrid_linear; the two
     biases share one dtype."""
-    N = gate.N
-    if N != up.N:
-        raise ValueError(f"the gate has {N} rows, the up projection {up.N}")
-    if bias_gate is not None and bias_up is not None and bias_gate.dtype != bias_up.dtype:
-        raise ValueError("bias_gate and bias_up must have one dtype")
-    dev, raw, M, x, xs = _product_input((gate, up), X, x_scales, stream)
-    bg, bu = _vector(bias_gate, N, dev, "bias_gate"), _vector(bias_up, N, dev, "bias_up")
-    bias = bias_gate if bias_gate is not None else bias_up
-    out, y_stride = _output(X, M, N, out, out_fp32, dev, stream)
-    code = load_library().patch_hybrid_gated(
-        gate.handle, up.handle, x, xs, M, out.data_ptr(), y_stride, 1 if out_fp32 else 0, bg, bu,
-        1 if bias is not None and bias.dtype is torch.float32 else 0, _activation(activation), raw)
-    _check("patch_hybrid_gated", code)
-    return out
-
-
-_NO_NORM = PatchNorm(0, 0, None, None, 0.0)
-
-
-def _norm(spec, C: int, dev, name: str) -> PatchNorm:
-    """(kind, weight, bias, eps) -> PatchNorm; None is no norm."""
-    if spec is None:
-        return _NO_NORM
-    kind, weight, bias, eps = spec
-    if kind not in NORMS:
-        raise ValueError(f"{name} norm {kind!r} is not one of {sorted(NORMS)}")
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError(f"{name}: weight and bias must have one dtype")
-    real = weight if weight is not None else bias
-    return PatchNorm(NORMS[kind], real is not None and real.dtype is torch.float32,
-                     _vector(weight, C, dev, f"{name} weight"), _vector(bias, C, dev, f"{name} bias"), eps)
+    return _run("patch_hybrid_gated", "gated", stream, gate._info, up._info, X, x_scales, bias_gate, bias_up,
+                _activation(activation), out, out_fp32)
 
 
 def patch_block_norm(branch: torch.Tensor, *, residual: torch.Tensor | None = None,
@@ -696,48 +594,12 @@ def patch_block_norm(branch: torch.Tensor, *, residual: torch.Tensor | None = No
     where there is a `pre` or z_type is "e4m3" (codes and a scale per token for
     patch_hybrid_linear's x_scales).  out_h and out_z may each be the residual
     or the branch (in place), not both the same.  Returns {"h", "z", "scales"}."""
-    dev, raw = _launch(branch, "branch", stream)
-    if branch.dim() != 2:
-        raise ValueError("branch must be [M, C]")
-    M, C = branch.shape
     if z_type not in Z_TYPES:
         raise ValueError(f"z_type {z_type!r} is not one of {sorted(Z_TYPES)}")
-    b, b_step = _rows(branch, M, C, _REAL, dev, "branch")
-    r, r_step = _rows(residual, M, C, _REAL, dev, "residual")
-    g, g_step, g_tokens = None, 0, 1
-    if gate is not None:
-        rows = 1 if gate.dim() == 1 else gate.shape[0]
-        if rows < 1 or M % rows:
-            raise ValueError(f"gate has {rows} rows, which do not divide {M} tokens")
-        g, g_step = _rows(gate if gate.dim() == 2 else gate.view(1, -1), rows, C, _REAL, dev, "gate")
-        g_tokens = max(M // rows, 1)
-    h_type = torch.float32 if h_fp32 else torch.bfloat16
-    if out_h is None:
-        out_h, h_step = _new(branch, (M, C), h_type, stream), C
-        h = out_h.data_ptr()
-    else:
-        h, h_step = _rows(out_h, M, C, (h_type,), dev, "out_h")
-    z = scales = s = None
-    z_step = 0
     want = Z_TYPES[z_type] if pre is not None or z_type == "e4m3" else 0
-    if want:
-        z_dtype = (torch.bfloat16, torch.float32, torch.uint8)[want - 1]
-        if out_z is None:
-            out_z, z_step = _new(branch, (M, C), z_dtype, stream), C
-            z = out_z.data_ptr()
-        else:
-            z, z_step = _rows(out_z, M, C, (z_dtype,), dev, "out_z")
-        if want == 3:
-            scales = _new(branch, (M,), torch.float32, stream)
-            s = scales.data_ptr()
-    elif out_z is not None:
-        raise ValueError("out_z without a pre norm")
-    args = PatchBlockNormArgs(b, b_step, r, r_step, g, g_step, g_tokens, h, h_step, z, z_step, s,
-                              _norm(post, C, dev, "post"), _norm(pre, C, dev, "pre"), scale,
-                              branch.dtype is torch.float32, r is not None and residual.dtype is torch.float32,
-                              g is not None and gate.dtype is torch.float32, h_fp32, want)
-    _check("patch_block_norm", load_library().patch_block_norm(ctypes.byref(args), M, C, raw))
-    return {"h": out_h, "z": out_z if want else None, "scales": scales}
+    h, z, scales = _run("patch_block_norm", "block_norm", stream, branch, residual, gate, scale, post, pre, want,
+                        h_fp32, out_h, out_z)
+    return {"h": h, "z": z, "scales": scales}
 
 
 def patch_free(packed: PackedWeight, stream=None) -> None:

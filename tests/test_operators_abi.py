@@ -93,5 +93,21 @@ def test_binding_refuses_host_tensors(P):
         P.patch_hybrid_linear(pk, x)
     with pytest.raises(ValueError, match="CUDA"):
         P.patch_hybrid_gated(pk, pk, x)
-    with pytest.raises(ValueError, match="one per handle"):
+    with pytest.raises(ValueError, match="CUDA"):
         P.patch_hybrid_linear_group([pk, pk], x, biases=[None])
+    for bad in (None, 3, [x]):
+        with pytest.raises(ValueError, match="tensor"):
+            P.patch_block_norm(bad)
+    with pytest.raises(ValueError, match="1 to 8"):
+        P.patch_hybrid_linear_group([], x)
+    with pytest.raises(ValueError, match="z_type"):
+        P.patch_block_norm(x, z_type="fp16")
+    with pytest.raises(ValueError, match="activation"):
+        P.patch_hybrid_gated(pk, pk, x, activation="tanh")
+
+
+def test_binding_fails_loudly_without_its_native_module(P, monkeypatch, tmp_path):
+    monkeypatch.setattr(P, "_native", None)
+    monkeypatch.setattr(P, "_HERE", str(tmp_path))
+    with pytest.raises(P.PatchLibraryError):
+        P.patch_block_norm(torch.zeros(2, 64, dtype=torch.bfloat16))

@@ -309,6 +309,12 @@ def test_refusals(P, gen):
             P.patch_hybrid_linear(*args)
     with pytest.raises(ValueError):
         P.patch_hybrid_linear(f8.packed, q, x_scales=s[:3])
+    with pytest.raises(ValueError, match="one per handle"):
+        P.patch_hybrid_linear_group([w.packed, w.packed], x, biases=[None])
+    closed = Weight(P, gen, 256, 256).packed
+    closed.close()
+    with pytest.raises(P.PatchError):
+        P.patch_hybrid_linear(closed, x)
     with pytest.raises(ValueError):
         P.patch_hybrid_gated(w.packed, tall.packed, x)
     with pytest.raises(ValueError):
