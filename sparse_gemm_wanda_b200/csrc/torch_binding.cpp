@@ -276,11 +276,11 @@ patch_norm norm_spec(PyObject *spec, int64_t C, c10::Device dev, const char *nam
     return s;
 }
 
-// block_norm(branch, residual, gate, scale, post, pre, z_type, h_fp32, out_h, out_z)
-// -> (h, z or None, scales or None)
+// block_norm(branch, residual, gate, scale, post, pre, z_type, want_h, h_fp32, out_h, out_z)
+// -> (h or None, z or None, scales or None)
 PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 10) refuse("block_norm: 10 arguments");
+    if (n != 11) refuse("block_norm: 11 arguments");
     const at::Tensor *branch = tensor(a[0], "branch"), *res = tensor(a[1], "residual"), *gate = tensor(a[2], "gate");
     const c10::Device dev = device_of(branch, "branch");
     if (branch->dim() != 2) refuse("branch must be [M, C]");
@@ -302,23 +302,28 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     p.post = norm_spec(a[4], C, dev, "post");
     p.pre = norm_spec(a[5], C, dev, "pre");
     p.z_type = static_cast<int32_t>(PyLong_AsLong(a[6]));
-    p.h_is_fp32 = PyObject_IsTrue(a[7]) == 1;
+    const bool want_h = PyObject_IsTrue(a[7]) == 1;
+    p.h_is_fp32 = PyObject_IsTrue(a[8]) == 1;
     if (PyErr_Occurred()) throw python_error();
     p.branch_is_fp32 = is_fp32(branch);
     p.residual_is_fp32 = is_fp32(res);
     p.gate_is_fp32 = is_fp32(gate);
     at::Tensor fresh;
-    THPObjectPtr h(output(a[8], M, C, p.h_is_fp32 ? at::kFloat : at::kBFloat16, dev, "out_h", &fresh, &p.h, &p.h_stride));
-    THPObjectPtr z, scales;
+    THPObjectPtr h, z, scales;
+    if (want_h)
+        h = THPObjectPtr(output(a[9], M, C, p.h_is_fp32 ? at::kFloat : at::kBFloat16, dev, "out_h", &fresh, &p.h,
+                                &p.h_stride));
+    else if (a[9] != Py_None)
+        refuse("out_h without want_h");
     if (p.z_type != PATCH_Z_NONE) {
         const at::ScalarType type = p.z_type == PATCH_Z_BF16 ? at::kBFloat16 : p.z_type == PATCH_Z_FP32 ? at::kFloat : at::kByte;
-        z = THPObjectPtr(output(a[9], M, C, type, dev, "out_z", &fresh, &p.z, &p.z_stride));
+        z = THPObjectPtr(output(a[10], M, C, type, dev, "out_z", &fresh, &p.z, &p.z_stride));
         if (p.z_type == PATCH_Z_E4M3) {
             at::Tensor s = at::empty({M}, at::TensorOptions().dtype(at::kFloat).device(dev));
             p.z_scales = s.mutable_data_ptr<float>();
             scales = THPObjectPtr(THPVariable_Wrap(s));
         }
-    } else if (a[9] != Py_None) {
+    } else if (a[10] != Py_None) {
         refuse("out_z without a pre norm");
     }
     void *stream = current_stream(dev);

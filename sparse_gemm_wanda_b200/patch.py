@@ -581,8 +581,9 @@ def patch_hybrid_gated(gate: PackedWeight, up: PackedWeight, X: torch.Tensor, *,
 
 def patch_block_norm(branch: torch.Tensor, *, residual: torch.Tensor | None = None,
                      gate: torch.Tensor | None = None, scale: float = 1.0, post: tuple | None = None,
-                     pre: tuple | None = None, z_type: str = "bf16", h_fp32: bool = False,
-                     out_h: torch.Tensor | None = None, out_z: torch.Tensor | None = None, stream=None) -> dict:
+                     pre: tuple | None = None, z_type: str = "bf16", want_h: bool = True,
+                     h_fp32: bool = False, out_h: torch.Tensor | None = None,
+                     out_z: torch.Tensor | None = None, stream=None) -> dict:
     """The boundary between two sublayers, one pass over the rows:
 
         h = residual + scale * gate * norm_post(branch),    z = norm_pre(h)
@@ -592,13 +593,14 @@ def patch_block_norm(branch: torch.Tensor, *, residual: torch.Tensor | None = No
     row).  post and pre are (kind, weight, bias, eps) with kind "rms" or
     "layer" and weight, bias [C] or None; post None means no norm.  z is given
     where there is a `pre` or z_type is "e4m3" (codes and a scale per token for
-    patch_hybrid_linear's x_scales).  out_h and out_z may each be the residual
-    or the branch (in place), not both the same.  Returns {"h", "z", "scales"}."""
+    patch_hybrid_linear's x_scales); h unless want_h is False (a norm alone).
+    out_h and out_z may each be the residual or the branch (in place), not both
+    the same.  Returns {"h", "z", "scales"}."""
     if z_type not in Z_TYPES:
         raise ValueError(f"z_type {z_type!r} is not one of {sorted(Z_TYPES)}")
     want = Z_TYPES[z_type] if pre is not None or z_type == "e4m3" else 0
     h, z, scales = _run("patch_block_norm", "block_norm", stream, branch, residual, gate, scale, post, pre, want,
-                        h_fp32, out_h, out_z)
+                        want_h, h_fp32, out_h, out_z)
     return {"h": h, "z": z, "scales": scales}
 
 

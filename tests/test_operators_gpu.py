@@ -456,6 +456,21 @@ def test_norm_strides_and_rows_behind(P, gen, shift):
         assert torch.equal(t, k)
 
 
+@pytest.mark.parametrize("M,C", [(3, 1000), (40, 77), (4096, 4096)])
+def test_norm_alone(P, gen, M, C):
+    # no residual stream is written: a plain norm, and a plain quantisation
+    b = randn(gen, M, C, dtype=BF)
+    pre = ("rms", randn(gen, C, dtype=BF), None, 1e-5)
+    got = P.patch_block_norm(b, pre=pre, want_h=False)
+    assert got["h"] is None and torch.equal(got["z"], P.patch_block_norm(b, pre=pre)["z"])
+    if C % 8 == 0:
+        e = P.patch_block_norm(b, z_type="e4m3", want_h=False)
+        q, s = P.patch_quantize_fp8(b)
+        assert torch.equal(e["z"], q) and torch.equal(e["scales"], s)
+    with pytest.raises(P.PatchError):
+        P.patch_block_norm(b, want_h=False)
+
+
 def test_norm_in_place(P, gen):
     M, C = 33, 1000
     pre = ("rms", randn(gen, C, dtype=BF), None, 1e-5)
