@@ -621,7 +621,7 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream) {
     //   13.8, the rows being too few for its start), with two norms on four
     //   chunks a thread, so more rows are under way (34.5 against 38.1).
     int threads, smem;
-    if (vec && AllBf16::fit(p) && p.C >= 1024 && values >= 12000000) {
+    if (vec && AllBf16::fit(p) && p.C >= 1024 && values >= 10000000) {
         if (p.post.kind != kNormNone && stream_teams<4, 768>(p, &threads, &smem) > 1)
             return run_stream<4, 768>(p, stream);
         if (stream_teams<2, 1024>(p, &threads, &smem) > 0) return run_stream<2, 1024>(p, stream);
