@@ -65,21 +65,28 @@ __device__ __forceinline__ float epi_bias(const Epilogue &e, int64_t n) {
     return e.bias ? load_real(e.bias, n, e.bias_fp32) : 0.0f;
 }
 
-// NV values to consecutive rows of a column, `ld` elements apart.
+// NV values of type T to or from consecutive rows of a column, `ld` elements
+// apart, the first `count` of them (whole chunks without predicates).
+template <class T, int NV, class Put>
+__device__ __forceinline__ void for_column(T *y, int64_t ld, int count, const Put &put) {
+    if (count >= NV) {
+#pragma unroll
+        for (int q = 0; q < NV; ++q) put(y[q * ld], q);
+    } else {
+#pragma unroll
+        for (int q = 0; q < NV; ++q)
+            if (q < count) put(y[q * ld], q);
+    }
+}
+
 template <int NV>
 __device__ __forceinline__ void store_column(void *Y, int64_t i, int64_t ld, int count, const float (&v)[NV],
                                              int fp32) {
-    if (fp32) {
-        float *y = static_cast<float *>(Y) + i;
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-            if (q < count) y[q * ld] = v[q];
-    } else {
-        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(Y) + i;
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-            if (q < count) y[q * ld] = __float2bfloat16_rn(v[q]);
-    }
+    if (fp32)
+        for_column<float, NV>(static_cast<float *>(Y) + i, ld, count, [&](float &y, int q) { y = v[q]; });
+    else
+        for_column<__nv_bfloat16, NV>(static_cast<__nv_bfloat16 *>(Y) + i, ld, count,
+                                      [&](__nv_bfloat16 &y, int q) { y = __float2bfloat16_rn(v[q]); });
 }
 
 // NV consecutive tokens m0 .. m0 + count - 1 (count <= NV) of output column n.
@@ -90,24 +97,15 @@ __device__ __forceinline__ void store_column(void *Y, int64_t i, int64_t ld, int
 template <int NV>
 __device__ __forceinline__ void epi_fetch(const Epilogue &e, int64_t N, int64_t m0, int64_t n, int count,
                                           uint32_t (&r)[NV]) {
-#pragma unroll
-    for (int q = 0; q < NV; ++q) r[q] = 0u;
-    if (e.mul) {
-        const float *src = e.mul + m0 * N + n;
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-            if (q < count) r[q] = __float_as_uint(src[q * N]);
-    } else if (e.residual && e.res_fp32) {
-        const float *src = static_cast<const float *>(e.residual) + m0 * e.ldr + n;
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-            if (q < count) r[q] = __float_as_uint(src[q * e.ldr]);
-    } else if (e.residual) {
-        const uint16_t *src = static_cast<const uint16_t *>(e.residual) + m0 * e.ldr + n;
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-            if (q < count) r[q] = src[q * e.ldr];
-    }
+    if (e.mul)
+        for_column<const float, NV>(e.mul + m0 * N + n, N, count,
+                                    [&](const float &x, int q) { r[q] = __float_as_uint(x); });
+    else if (e.residual && e.res_fp32)
+        for_column<const float, NV>(static_cast<const float *>(e.residual) + m0 * e.ldr + n, e.ldr, count,
+                                    [&](const float &x, int q) { r[q] = __float_as_uint(x); });
+    else if (e.residual)
+        for_column<const uint16_t, NV>(static_cast<const uint16_t *>(e.residual) + m0 * e.ldr + n, e.ldr, count,
+                                       [&](const uint16_t &x, int q) { r[q] = x; });
 }
 
 template <int NV>
@@ -116,11 +114,16 @@ __device__ __forceinline__ void epi_store(const Epilogue &e, void *Y, int y_fp32
 #pragma unroll
     for (int q = 0; q < NV; ++q) v[q] += bias;
     activate(v, e.act);
-    const int shift = e.mul || e.res_fp32 ? 0 : 16;
+    if (e.mul) {
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-        const float a = __uint_as_float(r[q] << shift);
-        v[q] = e.mul ? v[q] * a : fmaf(e.alpha, v[q], a);
+        for (int q = 0; q < NV; ++q) v[q] *= __uint_as_float(r[q]);
+    } else if (e.residual) {
+        const int shift = e.res_fp32 ? 0 : 16;
+#pragma unroll
+        for (int q = 0; q < NV; ++q) v[q] = fmaf(e.alpha, v[q], __uint_as_float(r[q] << shift));
+    } else {
+#pragma unroll
+        for (int q = 0; q < NV; ++q) v[q] *= e.alpha;
     }
     store_column(Y, m0 * e.ldy + n, e.ldy, count, v, y_fp32);
 }
@@ -132,15 +135,18 @@ template <class Sums>
 __device__ __forceinline__ void epi_drain(const Epilogue &e, void *Y, int y_fp32, int64_t N, int c, int step,
                                           int64_t m_base, int m_valid, int64_t n, float bias, uint32_t (&add)[16],
                                           const Sums &sums) {
+    const bool reads = e.mul || e.residual;
 #pragma unroll 1
     for (; c < m_valid; c += step) {
         float v[16];
         uint32_t next[16];
         sums(c, v);
-        epi_fetch(e, N, m_base + c + step, n, m_valid - c - step, next);
+        if (reads) epi_fetch(e, N, m_base + c + step, n, m_valid - c - step, next);
         epi_store(e, Y, y_fp32, m_base + c, n, m_valid - c, bias, v, add);
+        if (reads) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) add[q] = next[q];
+            for (int q = 0; q < 16; ++q) add[q] = next[q];
+        }
     }
 }
 
