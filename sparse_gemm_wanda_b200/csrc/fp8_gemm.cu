@@ -43,6 +43,10 @@ namespace patchk {
 namespace {
 
 constexpr int kF8Threads = 224;
+// products with an epilogue: + a second group of four epilogue warps (7-10),
+// the two taking alternate 16-column chunks (a short K is bound by them)
+template <bool EPI>
+constexpr int kF8Block = kF8Threads + (EPI ? 128 : 0);
 constexpr int kF8Step = 128;                 // columns (bytes of codes) per k-step
 constexpr int kF8Aslot = kDenseStepBytes;    // 16 KB: a dense k-step, or metadata + kept codes
 constexpr int kF8SmemLimit = 232448;
@@ -95,7 +99,7 @@ struct F8Cfg {
 };
 
 template <int BN, bool EPI>
-__global__ void __launch_bounds__(kF8Threads, 1)
+__global__ void __launch_bounds__(kF8Block<EPI>, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ F8Params p) {
     using C = F8Cfg<BN>;
     constexpr int S = C::kStages;
@@ -122,7 +126,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], EPI ? 8 : 4);  // epilogue warps
         }
         *never_flag = 0u;
         *abort_flag = (*reinterpret_cast<volatile uint32_t *>(p.status) & kStatusTimeout) ? 1u : 0u;
@@ -269,6 +273,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         // ------------------------------------------------------- epilogue
         pdl_wait();  // Y and the partial slots may still be used by earlier kernels
         const int quad = warp % 4;
+        const int c_first = EPI && warp >= 7 ? 16 : 0;  // the second group's first chunk
+        constexpr int kChunkStep = EPI ? 32 : 16;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
         for (int i = 0;; ++i) {
@@ -292,7 +298,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 // this range's accumulator, unscaled, into the item's slot
                 float *part = p.partial + static_cast<int64_t>(w) * BN * kBand + row;
 #pragma unroll 1
-                for (int c0 = 0; c0 < m_valid; c0 += 16) {
+                for (int c0 = c_first; c0 < m_valid; c0 += kChunkStep) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
                     tmem_ld_wait();
@@ -303,7 +309,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             } else if (*abort_flag != 0) {
             } else if constexpr (EPI) {
                 uint32_t add[16];
-                epi_fetch(p.epi, p.N, m_base, n, m_valid, add);
+                epi_fetch(p.epi, p.N, m_base + c_first, n, m_valid - c_first, add);
                 auto scaled = [&](int c0, float(&v)[16]) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
@@ -315,10 +321,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     for (int q = 0; q < 16; ++q)
                         v[q] = __uint_as_float(r[q]) * swn * __shfl_sync(0xFFFFFFFFu, sxl, q);
                 };
-                epi_drain(p.epi, p.Y, p.y_fp32, p.N, 0, 16, m_base, m_valid, n, epi_bias(p.epi, n), add, scaled);
+                epi_drain(p.epi, p.Y, p.y_fp32, p.N, c_first, kChunkStep, m_base, m_valid, n, epi_bias(p.epi, n), add,
+                          scaled);
             } else {
 #pragma unroll 1
-                for (int c0 = 0; c0 < m_valid; c0 += 16) {
+                for (int c0 = c_first; c0 < m_valid; c0 += kChunkStep) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
                     tmem_ld_wait();
@@ -472,7 +479,7 @@ cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t kcfg = {};
     kcfg.gridDim = dim3(static_cast<unsigned>(grid));
-    kcfg.blockDim = dim3(kF8Threads);
+    kcfg.blockDim = dim3(kF8Block<EPI>);
     kcfg.dynamicSmemBytes = C::kSmem;
     kcfg.stream = stream;
     kcfg.attrs = attr;
@@ -530,10 +537,10 @@ bool duo_fits(const Fp8Launch &g) {
 
 // Estimated time (us) of one product of more than 64 tokens with an epilogue
 // on the one-band kernel with its partials; duo_fp8_us the two-SM kernel's
-// (`pieces` of it a work item).  Fitted to calls in a graph on B200, f = 0.5, X quantised (us,
-// one-band / two-SM): 256x8192 M = 129 10.6 / 26.7, 1024x8192 M = 300 18.1 /
-// 28.5, 512x4096 M = 512 15.9 / 20.7, 4096x4096 M = 300 33.5 / 20.4,
-// 2048x1024 M = 512 22.1 / 14.0, M = 1024 20.2 / 14.9.
+// (`pieces` of it a work item).  Fitted to calls in a graph on B200, f = 0.5,
+// X quantised (us, one-band / two-SM): 256x8192 M = 129 10.6 / 25, 1024x8192
+// M = 300 18 / 27.6, 512x4096 M = 512 15.9 / 20.2, 4096x4096 M = 300 33.7 /
+// 18.7, M = 512 22.4 / 20.2.
 double one_band_fp8_us(const Fp8Launch &g) {
     const int bn = g.M <= 128 ? 128 : 240;
     const int64_t tiles = (g.N / kBand) * ((g.M + bn - 1) / bn);
@@ -542,15 +549,15 @@ double one_band_fp8_us(const Fp8Launch &g) {
     split_tiles(g, static_cast<int>(tiles), static_cast<int>(g.K / kF8Step), &ksplit, &kper);
     const int64_t rounds = (tiles * ksplit + g.num_sms - 1) / g.num_sms;
     const double partial_mb = ksplit > 1 ? 4e-6 * static_cast<double>(g.M) * static_cast<double>(g.N) * ksplit : 0.0;
-    // unsplit, a tile's own epilogue: four warps storing bn columns
-    const double store = ksplit > 1 ? 0.0 : static_cast<double>(rounds * bn) / 30.0;
+    // unsplit, a tile's own epilogue of bn columns
+    const double store = ksplit > 1 ? 0.0 : static_cast<double>(rounds * bn) / 60.0;
     return 8.5 + 0.45 * static_cast<double>(rounds * kper) + partial_mb / 3.0 + store;
 }
 
 }  // namespace
 
 double duo_fp8_us(const Fp8Launch &g, const DuoFp8Plan &dp, int pieces) {
-    return 11.0 + pieces * dp.cost * static_cast<double>(g.K / kF8Step) / 1750.0;
+    return 10.4 + pieces * dp.cost * static_cast<double>(g.K / kF8Step) / 1750.0;
 }
 
 bool takes_duo_fp8(const Fp8Launch &g) {

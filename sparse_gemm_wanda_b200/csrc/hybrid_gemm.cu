@@ -68,6 +68,11 @@ namespace patchk {
 
 constexpr int kGemmThreads = 192;
 constexpr int kGemmThreadsNM = 448;  // + 8 converter warps for 4:8 handles
+// products with an epilogue: + a second group of four epilogue warps, the two
+// taking alternate 16-column chunks (a short K is bound by them)
+constexpr int kGemmEpiThreads = 128;
+template <bool NM, bool EPI>
+constexpr int kGemmBlock = (NM ? kGemmThreadsNM : kGemmThreads) + (EPI ? kGemmEpiThreads : 0);
 constexpr int kConvWarps = 8;
 constexpr int kLutBytes = 256 * 32;  // per keep mask: 4 byte-permute selectors, 4 zero masks
 // k-steps of one segment whose table entries are staged in shared memory
@@ -223,7 +228,7 @@ __device__ __forceinline__ void fence_async_shared() {
 }
 
 template <int BN, int STAGES, bool NM, bool EPI>
-__global__ void __launch_bounds__(NM ? kGemmThreadsNM : kGemmThreads, 1)
+__global__ void __launch_bounds__(kGemmBlock<NM, EPI>, 1)
 hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ GemmParams p) {
     using C = GemmCfg<BN, STAGES>;
     extern __shared__ uint8_t smem_raw[];
@@ -266,7 +271,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], EPI ? 8 : 4);  // epilogue warps
             mbar_init(&tab_full[b], 1);
         }
         *never_flag = 0u;
@@ -474,7 +479,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 atomicOr(p.status, kStatusTimeout);
             }
         }
-    } else if (warp >= 6) {
+    } else if (NM && warp >= 6 && warp < 6 + kConvWarps) {
         if constexpr (NM) {
             if (!skip) {
                 // -------------------------------------------- 4:8 converters
@@ -523,6 +528,8 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         // ------------------------------------------------------- epilogue
         pdl_wait();  // Y and the partials may still be in use by earlier kernels
         const int quad = warp % 4;  // TMEM lanes 32*quad .. 32*quad+31
+        const int c_first = EPI && warp >= 6 ? 16 : 0;  // the second group's first chunk
+        constexpr int kChunkStep = EPI ? 32 : 16;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
         Segment sg;
@@ -547,7 +554,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             if constexpr (EPI) {
                 if (whole && live) {
                     uint32_t add[16];
-                    epi_fetch(p.epi, p.N, m_base, n, m_valid, add);
+                    epi_fetch(p.epi, p.N, m_base + c_first, n, m_valid - c_first, add);
                     auto sums = [&](int c0, float(&v)[16]) {
                         uint32_t r[16];
                         tmem_ld_32x32b_x16(lane_base + buf * BN + c0, r);
@@ -555,11 +562,12 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 #pragma unroll
                         for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
                     };
-                    epi_drain(p.epi, p.Y, p.y_fp32, p.N, 0, 16, m_base, m_valid, n, epi_bias(p.epi, n), add, sums);
+                    epi_drain(p.epi, p.Y, p.y_fp32, p.N, c_first, kChunkStep, m_base, m_valid, n, epi_bias(p.epi, n),
+                              add, sums);
                 }
             }
 #pragma unroll 1
-            for (int c0 = 0; c0 < (whole ? 0 : BN); c0 += 16) {
+            for (int c0 = c_first; c0 < (whole ? 0 : BN); c0 += kChunkStep) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(lane_base + buf * BN + c0, r);
                 tmem_ld_wait();
@@ -784,7 +792,7 @@ cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) 
     // before griddepcontrol.wait)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(NM ? kGemmThreadsNM : kGemmThreads);
+    cfg.blockDim = dim3(kGemmBlock<NM, EPI>);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -842,10 +850,10 @@ namespace {
 // for plain products, kept there with their results) miss what a call costs
 // before its first and after its last k-step, and that the one-band kernel
 // spreads few tiles over every SM.  Fitted to calls in a graph on B200, f = 0.5
-// (us, one-band / two-SM): 256x8192 M = 129 15.3 / 35.9, 1024x8192 M = 512
-// 23.8 / 36.5, 512x4096 M = 300 15.1 / 21.3, 1024x2048 M = 300 16.2 / 13.9,
-// 4096x1024 M = 100 15.4 / 9.9, 4096x4096 M = 100 18.2 / 21.2, M = 200 27.9 /
-// 21.6; band-pair 4096x4096 M = 129 48.7, 4096x1024 M = 300 21.4.
+// (us, one-band / two-SM): 256x8192 M = 129 15 / 34.6, 1024x8192 M = 512 24 /
+// 35.8, 512x4096 M = 300 15 / 20.3, 1024x2048 M = 300 16 / 12.7, 4096x1024
+// M = 100 15 / 9, 4096x4096 M = 100 18 / 20.2, M = 200 27.6 / 20.5; band-pair
+// 4096x4096 M = 129 42, 1024x2048 M = 512 23.7.
 struct Choice {
     int kernel = 1;  // 1 one band, 2 band pair, 3 two-SM
     double us = 0;
@@ -855,7 +863,7 @@ struct Choice {
 constexpr double kCyclesPerUs = 1750.0;
 
 double duo_us(const DuoPlan &dp, int64_t K, int pieces) {
-    return 6.3 + pieces * dp.cost * static_cast<double>(K / kStep) / kCyclesPerUs;
+    return 5.3 + pieces * dp.cost * static_cast<double>(K / kStep) / kCyclesPerUs;
 }
 
 Choice choose_kernel(const GemmLaunch &g) {
@@ -874,7 +882,8 @@ Choice choose_kernel(const GemmLaunch &g) {
         }
     }
     const PairPlan pp = plan_pair_gemm(g.N, g.M, g.num_sms);
-    const double us = 12.0 + pp.cost * static_cast<double>(g.K / kStep) / 2100.0;
+    // 0.58 us a k-step whatever the tile: bound by its copies and its issue
+    const double us = 6.0 + 0.58 * pp.waves * static_cast<double>(g.K / kStep);
     if (us < c.us) {
         c.kernel = 2;
         c.us = us;
