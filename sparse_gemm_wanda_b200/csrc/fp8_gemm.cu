@@ -421,6 +421,21 @@ void split_tiles(const Fp8Launch &g, int tiles, int steps, int *ksplit, int *kpe
             *ksplit = (steps + *kper - 1) / *kper;
         }
     }
+    if (!g.epi_on || *ksplit == 1) return;
+    // With an epilogue: whole tiles all the same where the fix-up is estimated
+    // to cost more than the k-steps it shares out.  Fitted to calls in a graph
+    // on B200, f = 0.5 (us, split / whole): 1152x256 M = 16 5.1 / 4.0, M = 1000
+    // 16.6 / 10.5, 2432x1024 M = 300 18.0 / 12.4, 1152x1024 M = 129 7.7 / 9.7,
+    // 384x2048 M = 16 5.6 / 8.2, M = 1000 13.0 / 14.8.
+    const double mn = 1e-6 * static_cast<double>(g.M) * static_cast<double>(g.N);
+    const double cols = static_cast<double>(std::min<int64_t>(g.M, g.M <= 64 ? 64 : g.M <= 128 ? 128 : 240));
+    const int rounds = (tiles * *ksplit + g.num_sms - 1) / g.num_sms;
+    const double whole = 3.0 + 0.03 * cols + 0.31 * steps;
+    const double split = 4.4 + 0.009 * cols + 0.3 * *kper + 1.6 * (rounds - 1) + mn * (8.5 + 0.67 * *ksplit);
+    if (whole <= split) {
+        *ksplit = 1;
+        *kper = steps;
+    }
 }
 
 template <int BN, bool EPI>

@@ -57,6 +57,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -735,6 +736,28 @@ void streamk_bounds(const GemmLaunch &g, GemmParams &p, int bn, int P) {
         if (p.u0[c] >= p.u0[c + 1]) p.u0[c] = p.u0[c + 1] - 1;
 }
 
+// Estimated time (us) of one product with an epilogue on the one-band kernel
+// with BN-token tiles, and whether whole tiles beat stream-K.  Whole tiles
+// cost the last wave's idle SMs; stream-K its fix-up, which reads and adds
+// every output's partials.  Fitted to calls in a graph on B200, f = 0.5 (us,
+// stream-K / whole): 384x512 M = 65 8.2 / 6.9, 384x2048 M = 65 8.8 / 12.9,
+// 1152x2048 M = 1000 26.3 / 14.5, 2432x1024 M = 300 18.5 / 10.2, 9600x2048
+// M = 129 28.2 / 15.1, M = 1000 43.0 / 43.0; 4:8 handles 1152x1024 M = 129
+// 12.3 / 15.0, 9600x1024 M = 129 40.6 / 23.9.
+struct OneBand {
+    double us;
+    bool whole;
+};
+OneBand one_band_estimate(const GemmLaunch &g, int bn, bool nm) {
+    const double sms = g.num_sms, pairs = static_cast<double>(g.K / (2 * kStep));
+    const double tiles = static_cast<double>((g.N / kBand) * ((g.M + bn - 1) / bn));
+    const double whole = 4.7 + std::ceil(tiles / sms) * ((nm ? 0.97 : 0.5) * pairs + bn * 1.5 / 160);
+    const double sharing = std::min(62.0, std::max(1.0, std::min(sms, tiles * pairs) / tiles));
+    const double stream = 9.5 + (nm ? 1.3 : 0.8) * std::ceil(tiles * pairs / sms) +
+                          1e-5 * static_cast<double>(g.M) * static_cast<double>(g.N) + 0.065 * sharing;
+    return tiles >= 2 * sms || whole <= stream ? OneBand{whole, true} : OneBand{stream, false};
+}
+
 template <int BN, int STAGES, bool NM, bool EPI>
 cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
     using C = GemmCfg<BN, STAGES>;
@@ -767,7 +790,8 @@ cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) 
     const int64_t tiles = static_cast<int64_t>(p.bands) * p.ttiles;
     const int64_t slots = static_cast<int64_t>(g.num_sms) * ctas_per_sm;
     // whole tiles when there are at least two waves of them, stream-K otherwise
-    const bool sk = tiles < 2 * slots;
+    // (with an epilogue: whole tiles also where they are estimated faster)
+    const bool sk = tiles < 2 * slots && !(EPI && one_band_estimate(g, BN, NM).whole);
     p.stream_k = sk ? 1 : 0;
     p.units = tiles * (p.nsteps / 2);
     // stream-K: at most 62 CTAs per tile, so a tile's partials fit the fix-up's slot list
@@ -850,10 +874,9 @@ namespace {
 // for plain products, kept there with their results) miss what a call costs
 // before its first and after its last k-step, and that the one-band kernel
 // spreads few tiles over every SM.  Fitted to calls in a graph on B200, f = 0.5
-// (us, one-band / two-SM): 256x8192 M = 129 15 / 34.6, 1024x8192 M = 512 24 /
-// 35.8, 512x4096 M = 300 15 / 20.3, 1024x2048 M = 300 16 / 12.7, 4096x1024
-// M = 100 15 / 9, 4096x4096 M = 100 18 / 20.2, M = 200 27.6 / 20.5; band-pair
-// 4096x4096 M = 129 42, 1024x2048 M = 512 23.7.
+// (us, one-band with stream-K / two-SM): 256x8192 M = 129 15 / 34.6, 1024x8192
+// M = 512 24 / 35.8, 512x4096 M = 300 15 / 20.3, 4096x4096 M = 100 18 / 20.2,
+// M = 200 27.6 / 20.5; band-pair 4096x4096 M = 129 42, 1024x2048 M = 512 23.7.
 struct Choice {
     int kernel = 1;  // 1 one band, 2 band pair, 3 two-SM
     double us = 0;
@@ -868,10 +891,7 @@ double duo_us(const DuoPlan &dp, int64_t K, int pieces) {
 
 Choice choose_kernel(const GemmLaunch &g) {
     Choice c;
-    const int64_t bn = g.M <= 128 ? 128 : 160;
-    const int64_t units = (g.N / kBand) * ((g.M + bn - 1) / bn) * (g.K / (2 * kStep));
-    c.us = (bn == 128 ? 10.5 : 11.5) + static_cast<double>((units + g.num_sms - 1) / g.num_sms) +
-           (bn == 128 ? 2e-6 : 6e-6) * static_cast<double>(g.M) * static_cast<double>(g.N);
+    c.us = one_band_estimate(g, g.M <= 128 ? 128 : 160, false).us;
     if (g.K / kStep > 448) return c;
     if (g.duo_ok) {
         const DuoPlan dp = plan_duo_gemm(g.N, g.M, g.num_sms, g.max_pair_bytes);
