@@ -572,9 +572,7 @@ cudaError_t run_stream(const BlockNormParams &p, cudaStream_t stream) {
     int threads = 0, smem = 0;
     const int teams = stream_teams<NV, MAXT>(p, &threads, &smem);
     if (teams < 1) return cudaErrorInvalidValue;
-    // per call: the limit belongs to the current device
-    const cudaError_t attr_err = cudaFuncSetAttribute(block_norm_stream_kernel<AllBf16, NV, MAXT>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+    const cudaError_t attr_err = allow_smem<block_norm_stream_kernel<AllBf16, NV, MAXT>>(kNormSmem);
     if (attr_err != cudaSuccess) return attr_err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(p.num_sms, (p.M + teams - 1) / teams)));

@@ -675,12 +675,7 @@ namespace {
 template <int BN, bool F8>
 cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, bool gated) {
     using C = DecCfg<BN>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(decode_gemm_kernel<BN, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        C::kSmemBytes);
-    });
+    const cudaError_t attr_err = allow_smem<decode_gemm_kernel<BN, F8>>(C::kSmemBytes);
     if (attr_err != cudaSuccess) return attr_err;
     if (count < 1 || count > kDecMaxGroup) return cudaErrorInvalidValue;
     const GemmLaunch &g = gs[0];

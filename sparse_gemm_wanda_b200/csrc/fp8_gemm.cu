@@ -441,12 +441,7 @@ void split_tiles(const Fp8Launch &g, int tiles, int steps, int *ksplit, int *kpe
 template <int BN, bool EPI>
 cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     using C = F8Cfg<BN>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(fp8_gemm_kernel<BN, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        C::kSmem);
-    });
+    const cudaError_t attr_err = allow_smem<fp8_gemm_kernel<BN, EPI>>(C::kSmem);
     if (attr_err != cudaSuccess) return attr_err;
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorInvalidValue;

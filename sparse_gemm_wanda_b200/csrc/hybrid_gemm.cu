@@ -761,14 +761,9 @@ OneBand one_band_estimate(const GemmLaunch &g, int bn, bool nm) {
 template <int BN, int STAGES, bool NM, bool EPI>
 cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
     using C = GemmCfg<BN, STAGES>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
     constexpr int kSmem = C::kSmemBytes + (NM ? kLutBytes : 0);
     static_assert(kSmem <= 232448, "shared memory per CTA");
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(hybrid_gemm_kernel<BN, STAGES, NM, EPI>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    });
+    const cudaError_t attr_err = allow_smem<hybrid_gemm_kernel<BN, STAGES, NM, EPI>>(kSmem);
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap map;
     if (!make_x_map(&map, g.X, g.M, g.K, BN)) return cudaErrorInvalidValue;

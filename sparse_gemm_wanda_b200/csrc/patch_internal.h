@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace patchk {
 
 // Counts kernels enqueued by the library (exported as patch_launch_count).
@@ -102,6 +104,21 @@ struct Epilogue {
     int act = kActNone;
     int bias_fp32 = 0, res_fp32 = 0;
 };
+
+// Lets Kernel use `bytes` of dynamic shared memory on the current device: set
+// once per device, since a function's attributes belong to one.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 struct GemmLaunch {
     const uint8_t *packed;

@@ -468,16 +468,10 @@ bool encode_rows(EncodeTiledFn enc, CUtensorMap *m, const void *base, uint64_t r
 }
 
 cudaError_t ensure_duo_attributes() {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        for (auto *kernel : {duo_gemm_kernel<kEpiPlain>, duo_gemm_kernel<kEpiLinear>, duo_gemm_kernel<kEpiGated>}) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDuoSmemLimit);
-            if (e != cudaSuccess) attr_err = e;
-        }
-    });
-    return attr_err;
+    cudaError_t e = allow_smem<duo_gemm_kernel<kEpiPlain>>(kDuoSmemLimit);
+    if (e == cudaSuccess) e = allow_smem<duo_gemm_kernel<kEpiLinear>>(kDuoSmemLimit);
+    if (e == cudaSuccess) e = allow_smem<duo_gemm_kernel<kEpiGated>>(kDuoSmemLimit);
+    return e;
 }
 
 // clusters of two CTAs that fit on the device at once with `smem` bytes each

@@ -502,16 +502,10 @@ bool encode_rows(EncodeTiledFn enc, CUtensorMap *m, const void *base, uint64_t r
 }
 
 cudaError_t ensure_attributes() {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        for (auto *kernel : {duo_fp8_kernel<kEpiPlain>, duo_fp8_kernel<kEpiLinear>, duo_fp8_kernel<kEpiGated>}) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kD8SmemLimit);
-            if (e != cudaSuccess) attr_err = e;
-        }
-    });
-    return attr_err;
+    cudaError_t e = allow_smem<duo_fp8_kernel<kEpiPlain>>(kD8SmemLimit);
+    if (e == cudaSuccess) e = allow_smem<duo_fp8_kernel<kEpiLinear>>(kD8SmemLimit);
+    if (e == cudaSuccess) e = allow_smem<duo_fp8_kernel<kEpiGated>>(kD8SmemLimit);
+    return e;
 }
 
 // clusters of two CTAs that fit on the device at once with `smem` bytes each

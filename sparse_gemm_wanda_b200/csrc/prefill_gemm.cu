@@ -444,15 +444,8 @@ PairPlan plan_pair_gemm(int64_t N, int64_t M, int num_sms) {
 }
 
 cudaError_t launch_pair_gemm(const GemmLaunch &g, const PairPlan &plan, cudaStream_t stream) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        for (auto *kernel : {pair_gemm_kernel<false>, pair_gemm_kernel<true>}) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgSmemLimit);
-            if (e != cudaSuccess) attr_err = e;
-        }
-    });
+    cudaError_t attr_err = allow_smem<pair_gemm_kernel<false>>(kPgSmemLimit);
+    if (attr_err == cudaSuccess) attr_err = allow_smem<pair_gemm_kernel<true>>(kPgSmemLimit);
     if (attr_err != cudaSuccess) return attr_err;
     if (plan.stages < 2 || plan.smem > kPgSmemLimit) return cudaErrorInvalidValue;
     EncodeTiledFn enc = encode_fn();

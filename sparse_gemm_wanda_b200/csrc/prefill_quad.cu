@@ -408,13 +408,7 @@ bool encode_rows(EncodeTiledFn enc, CUtensorMap *m, const void *base, uint64_t r
 }
 
 cudaError_t ensure_quad_attributes() {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(quad_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kQdSmemLimit);
-    });
-    return attr_err;
+    return allow_smem<quad_gemm_kernel>(kQdSmemLimit);
 }
 
 // clusters of two CTAs that fit on the device at once with `smem` bytes each
