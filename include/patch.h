@@ -510,8 +510,8 @@ typedef struct {
  * concurrently (the rule of patch_hybrid_gemm), graphs that hold them
  * included.  Errors: INVALID_ARG (null or misaligned pointers, a stride below
  * N, an activation outside the list, x_scales on a handle that is not FP8, a
- * handle of another device, Y at the residual's address with another stride
- * or type), OOM, CUDA.
+ * handle of another device, Y at X's address, or at the residual's with
+ * another stride or type), OOM, CUDA.
  */
 patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const float *x_scales,
                                  int64_t M, void *Y, int32_t y_is_fp32, const patch_epilogue *epi,
@@ -598,8 +598,9 @@ typedef struct {
  * codes come from the fp32 values, not from values rounded to bf16 first.
  *
  *   M  rows, >= 0 (0 returns PATCH_OK without touching anything).
- *   C  1 .. 32768, any value (multiples of 8 with 16-byte aligned pointers and
- *      strides take 16-byte accesses).
+ *   C  1 .. 32768, any value.  Rows take wide accesses where C is a multiple
+ *      of 8 and every bf16 row, weight and gate starts on 16 bytes, every
+ *      fp32 one on 32, the codes' on 8.
  *
  * h and z may each be the residual or the branch itself, not both the same one
  * (same address, stride and type); no other overlap.  Stream-ordered, no

@@ -1284,7 +1284,10 @@ patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t c
         st = check_epilogue(epis ? epis + i : nullptr, Wps[i]->shp.N, M, Ys[i], y_is_fp32, &es[i]);
         if (st != PATCH_OK) return st;
     }
-    // the members run in no order: none may write what another writes or reads
+    // the members run in no order: none may write what another writes or
+    // reads, and X is read to the end
+    for (int i = 0; i < count && M > 0; ++i)
+        if (Ys[i] == X) return PATCH_ERR_INVALID_ARG;
     for (int i = 0; i < count && M > 0; ++i)
         for (int j = 0; j < count; ++j)
             if (i != j && (Ys[i] == Ys[j] || Ys[i] == es[j].residual)) return PATCH_ERR_INVALID_ARG;
@@ -1313,6 +1316,7 @@ patch_status patch_hybrid_gated(const patch_packed *Wgate, const patch_packed *W
     if (st != PATCH_OK) return st;
     if (!aligned_to(bias_up, real_bytes(bias_is_fp32))) return PATCH_ERR_INVALID_ARG;
     if (M == 0) return PATCH_OK;
+    if (Y == X) return PATCH_ERR_INVALID_ARG;
     patchk::Epilogue up;
     up.bias = bias_up;
     up.bias_fp32 = bias_is_fp32;

@@ -676,3 +676,122 @@ def test_norm_many_rows(P, gen, M, C):
     keep = wide_r[:, C:].clone()
     got = P.patch_block_norm(wide_b[:, :C], residual=wide_r[:, :C], out_h=wide_r[:, :C])
     assert torch.equal(got["h"], want["h"]) and torch.equal(wide_r[:, C:], keep)
+
+
+@pytest.mark.parametrize("kind,kernel,M", [("2:4", 0, 8), ("fp8", 0, 8), ("2:4", 1, 300), ("2:4", 2, 300), ("2:4", 3, 300),
+                                           ("4:8", 0, 100)])
+def test_a_wait_that_runs_out_raises_the_status(P, gen, kind, kernel, M):
+    # a k-step that never lands ends every form of a product through its
+    # bounded waits; the status is read and cleared, and the next call is right
+    # (the kernels that have the hook: all but the FP8 prefill ones)
+    wg, wu = Weight(P, gen, 512, 512, kind), Weight(P, gen, 512, 512, kind)
+    x, _ = x_of(gen, wg, M)
+    res = randn(gen, M, 512, dtype=BF)
+
+    def calls():
+        yield P.patch_hybrid_linear(wg.packed, x, activation="silu", residual=res)
+        yield P.patch_hybrid_gated(wg.packed, wu.packed, x)
+
+    P.test_prefill_kernel(kernel)
+    try:
+        for i in range(2):
+            P.test_stall_first_kstep(True)
+            try:
+                next(c for k, c in enumerate(calls()) if k == i)
+            finally:
+                P.test_stall_first_kstep(False)
+            assert P.patch_get_status(wg.packed) == 5  # PATCH_ERR_TIMEOUT
+            P.patch_get_status(wu.packed)
+        y, z = calls()
+        torch.cuda.synchronize()
+    finally:
+        P.test_prefill_kernel(0)
+    assert P.patch_get_status(wg.packed) == 0 and P.patch_get_status(wu.packed) == 0
+    check_linear(y, wg, x, act="silu", residual=res)
+    check_gated(z, wg, wu, x)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+@pytest.mark.parametrize("kind", ["2:4", "fp8"])
+def test_rows_beyond_32_bit_offsets(P, gen, kind, kernel):
+    # rows so far apart that the last ones start above 2^31 elements
+    M, N, step = 2100, 256, (1 << 20) + 8
+    wg, wu = Weight(P, gen, N, 256, kind), Weight(P, gen, N, 256, kind)
+    x, _ = x_of(gen, wg, M)
+    stream = torch.empty(M * step, dtype=BF, device="cuda").view(M, step)[:, 16:16 + N]
+    res = randn(gen, M, N, dtype=BF)
+    stream.copy_(res)
+    P.test_prefill_kernel(kernel)
+    try:
+        check_linear(P.patch_hybrid_linear(wg.packed, x, residual=stream, out=stream), wg, x, residual=res)
+        check_gated(P.patch_hybrid_gated(wg.packed, wu.packed, x, out=stream), wg, wu, x)
+    finally:
+        P.test_prefill_kernel(0)
+    del stream
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M,C,step", [(2100, 520, (1 << 20) + 8), (2100, 333, (1 << 20) + 5), (10000, 1024, 1 << 18)])
+def test_norm_rows_beyond_32_bit_offsets(P, gen, M, C, step):
+    b, r = randn(gen, M, C, dtype=BF), randn(gen, M, C, dtype=BF)
+    pre = ("rms", randn(gen, C, dtype=BF), None, 1e-5)
+    wide = torch.empty(M * step, dtype=BF, device="cuda").view(M, step)
+    views = [wide[:, i * C:(i + 1) * C] for i in range(3)] if C % 8 else [wide[:, i * 2048:i * 2048 + C] for i in range(3)]
+    views[0].copy_(b)
+    views[1].copy_(r)
+    check_norm(P, views[0], views[1], pre=pre, out_h=views[1], out_z=views[2])
+    del wide, views
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("shift", [4, 8])
+def test_norm_fp32_rows_on_16_and_32_byte_boundaries(P, gen, shift):
+    M, C = 9, 256
+    big = [randn(gen, M, C + 16) for _ in range(4)]
+    b, r, h, z = [t[:, shift:shift + C] for t in big]
+    wt = randn(gen, C + 8)[shift:shift + C]
+    check_norm(P, b, r, post=("rms", wt, None, 1e-5), pre=("layer", wt, wt, 1e-5), z_type="fp32", h_fp32=True, out_h=h,
+               out_z=z)
+
+
+@pytest.mark.parametrize("kind", ["2:4", "fp8"])
+@pytest.mark.parametrize("M", [1, 50, 100, 300])
+def test_eight_members(P, gen, kind, M):
+    ws = [Weight(P, gen, 128 * (1 + i % 3), 256, kind) for i in range(8)]
+    x, _ = x_of(gen, ws[0], M)
+    biases = [randn(gen, w.N) for w in ws]
+    for y, w, b in zip(P.patch_hybrid_linear_group([w.packed for w in ws], x, biases=biases, activation="relu"), ws, biases):
+        check_linear(y, w, x, bias=b, act="relu")
+
+
+@pytest.mark.parametrize("kind", ["2:4", "fp8", "4:8"])
+@pytest.mark.parametrize("M", [4, 300])
+def test_two_streams_at_once(P, gen, kind, M):
+    # different handles on different streams share nothing
+    blocks = [Block(P, gen, kind) for _ in range(2)]
+    attn, res = randn(gen, M, 256, dtype=BF), randn(gen, M, 256, dtype=BF)
+    want = [[t.clone() for t in b(attn, res.clone())[1:]] for b in blocks]
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (b, s) in enumerate(zip(blocks, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(b(attn, res.clone())[1:])
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for run in runs:
+            assert all(torch.equal(u, v) for u, v in zip(w, run))
+
+
+def test_an_output_on_top_of_the_input_is_refused(P, gen):
+    w = Weight(P, gen, 256, 256)
+    for M in (3, 300):
+        x, _ = x_of(gen, w, M)
+        keep = x.clone()
+        for call in (lambda: P.patch_hybrid_linear(w.packed, x, out=x), lambda: P.patch_hybrid_gated(w.packed, w.packed, x, out=x),
+                     lambda: P.patch_hybrid_linear_group([w.packed, w.packed], x, outs=[None, x])):
+            with pytest.raises(P.PatchError):
+                call()
+        torch.cuda.synchronize()
+        assert torch.equal(x, keep)
