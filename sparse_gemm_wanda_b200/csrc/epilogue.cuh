@@ -3,7 +3,9 @@
 //
 // A product's last kernel (the GEMM, or the fix-up that joins its partials)
 // holds every sum in a register of the thread that stores it, so the epilogue
-// costs one read of the residual and no pass of its own.
+// costs one read of the residual and no pass of its own (4096x11008, M = 512,
+// residual: 56 us, against 67.5 with a kernel of its own over fp32 sums and
+// 48-50 for the product alone).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -24,7 +26,7 @@ __device__ __forceinline__ float act_gelu(float v) { return 0.5f * v * (1.0f + e
 // x / (1 + exp(-y)) by the hardware's exponential and reciprocal: off by at most
 // about 2^-21 + 2^-24 |y| of the result, against 2^-9 for a bf16 output.  Eight
 // warps finish an accumulator, so a short K is bound by these instructions
-// (FP8, 2478 tokens, 7168x256 gated: 77 us with tanhf).
+// (FP8, 2478 tokens, 7168x256 gated: 66 us, 77 with tanhf).
 __device__ __forceinline__ float over_one_plus_exp(float x, float y) { return __fdividef(x, 1.0f + __expf(-y)); }
 // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u))
 __device__ __forceinline__ float act_gelu_tanh(float v) {
