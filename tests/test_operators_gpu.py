@@ -795,3 +795,35 @@ def test_an_output_on_top_of_the_input_is_refused(P, gen):
                 call()
         torch.cuda.synchronize()
         assert torch.equal(x, keep)
+
+
+@pytest.mark.parametrize("C", [515, 1001, 4100, 5247, 8186, 8193, 13491, 16381, 16385, 30001, 32761, 32767])
+@pytest.mark.parametrize("M", [1, 11, 300])
+def test_norm_rows_between_boundaries(P, gen, C, M):
+    # rows that start at every place between two 16-byte boundaries
+    bf = dict(dtype=BF)
+    rms = ("rms", randn(gen, C, spread=0.2, **bf) + 1, None, 1e-5)
+    layer = ("layer", randn(gen, C, **bf), randn(gen, C, **bf), 1e-5)
+    check_norm(P, randn(gen, M, C, **bf), randn(gen, M, C, **bf), pre=rms)
+    check_norm(P, randn(gen, M, C, **bf), randn(gen, M, C), gate=randn(gen, C, **bf), post=layer, pre=rms, z_type="e4m3",
+               h_fp32=True)
+    f32 = ("rms", randn(gen, C), None, 1e-5)
+    check_norm(P, randn(gen, M, C), randn(gen, M, C), post=f32, pre=rms, z_type="fp32")
+    check_norm(P, randn(gen, M, C), None, gate=randn(gen, M, C, **bf), pre=layer)
+
+
+@pytest.mark.parametrize("C,step", [(1001, 1003), (1000, 1003), (5000, 5001), (9001, 9008)])
+def test_norm_wide_rows_between_boundaries_in_place(P, gen, C, step):
+    # in place, rows further apart than C, nothing around them moves; the
+    # tensors' places agree in the first two calls and differ in the third
+    M = 21
+    pre = ("rms", randn(gen, C, dtype=BF), None, 1e-5)
+    for shifts in ((0, 0, 0), (3, 3, 3), (3, 1, 2)):
+        big = [randn(gen, M + 1, step + 8 - step % 8 + step % 8, dtype=BF).view(-1)[: M * step + 8] for _ in range(3)]
+        view = [t[k: k + M * step].view(M, step)[:, :C] for t, k in zip(big, shifts)]
+        keep = [t.clone() for t in big]
+        check_norm(P, view[0], view[1], scale=0.5, pre=pre, out_h=view[1], out_z=view[2])
+        assert torch.equal(big[0], keep[0])
+        for i in (1, 2):
+            keep[i][shifts[i]: shifts[i] + M * step].view(M, step)[:, :C] = view[i]
+            assert torch.equal(big[i], keep[i])
