@@ -14,9 +14,8 @@
 //
 // All loads of a row are issued before the first value is used (PREFETCH; with
 // four chunks a thread the residual is read late, for registers).  Rows whose width,
-// addresses or strides do not allow 16-byte accesses from their start take the
-// same kernel with chunks that begin at the boundary before it (kShifted), or
-// with one value per access, neighbouring threads on neighbouring values.
+// addresses or strides do not allow 16-byte accesses take the same kernel with
+// one value per access, neighbouring threads on neighbouring values.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -61,59 +60,45 @@ using AllBf16 = Types<kBf16, kBf16, kBf16>;
 using Fp32Stream = Types<kBf16, kFp32, kBf16>;  // a residual stream held in fp32
 using AnyTypes = Types<kRun, kRun, kRun>;
 
-// How the rows are accessed: one value at a time; 8 at a time; or 8 at a time
-// from the 8-element boundary before the row's start on, `phase` elements
-// before it (the same for every tensor of M rows), the chunks at the row's two
-// ends one value at a time.
-enum Access { kSingle = 0, kWide = 1, kShifted = 2 };
-
 // Thread t's place in a row of C values: chunk i holds the 8 values from at(i)
-// on, or (kSingle) at(i), at(i) + threads, ...
-template <Access A>
+// on (VEC), or at(i), at(i) + 32, ...: a warp's 8 accesses then cover 256
+// consecutive values at offsets known at compile time (with offsets in
+// multiples of the team's threads 1541x8585 took 51.6 us in place of 37.7,
+// 777x1001 with two layer norms 9.1 in place of 7.1).
+template <bool VEC>
 struct Place {
-    int t, threads, C, phase;
+    int t, threads, C;
+    static constexpr int step = VEC ? 1 : 32;
     __device__ __forceinline__ int at(int i) const {
-        if constexpr (A == kSingle) return i * 8 * threads + t;
-        return (i * threads + t) * 8 - (A == kShifted ? phase : 0);
+        return VEC ? (i * threads + t) * 8 : (i * threads + (t & ~31)) * 8 + (t & 31);
     }
     __device__ __forceinline__ bool has(int i) const { return at(i) < C; }
-    // whether all of a chunk lies inside the row (known where it is not asked per chunk)
-    __device__ __forceinline__ bool whole(int i) const {
-        if constexpr (A == kShifted) return at(i) >= 0 && at(i) + 8 <= C;
-        return A == kWide;
-    }
-    __device__ __forceinline__ bool in(int i, int k) const {
-        if constexpr (A == kSingle) return at(i) + k * threads < C;
-        if constexpr (A == kShifted) return at(i) + k >= 0 && at(i) + k < C;
-        return has(i);
-    }
-    __device__ __forceinline__ int step() const { return A == kSingle ? threads : 1; }
+    __device__ __forceinline__ bool in(int i, int k) const { return VEC ? has(i) : at(i) + k * step < C; }
+    // whether all 8 values lie inside the row
+    __device__ __forceinline__ bool full(int i) const { return VEC ? has(i) : at(i) + 7 * step < C; }
 };
 
-// 8 values as stored: fp32 one a word; bf16 two a word where `PAIRS`, else one
+// 8 values as stored: fp32 one a word; bf16 two a word (VEC) or one
 struct Raw {
     uint32_t w[8];
 };
-template <Access A>
-constexpr bool kPairs = A != kSingle;
 
-// one at a time, zeros outside the row
-template <class T, Access A>
-__device__ __forceinline__ void load_singles(const T *q, const Place<A> &a, int i, Raw &r) {
+// zeros outside the row
+template <class T>
+__device__ __forceinline__ void load_singles(const T *q, const Place<false> &a, int i, Raw &r) {
+    if (a.full(i)) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r.w[k] = a.in(i, k) ? q[k * a.step()] : 0u;
+        for (int k = 0; k < 8; ++k) r.w[k] = q[k * a.step];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r.w[k] = a.in(i, k) ? q[k * a.step] : 0u;
+    }
 }
 
-__device__ __forceinline__ void pack_pairs(Raw &r) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r.w[k] = r.w[2 * k] | (r.w[2 * k + 1] << 16);
-}
-
-// chunk i of a row of one of the tensors of M rows
-template <Access A>
-__device__ __forceinline__ void load8(const void *p, int64_t base, const Place<A> &a, int i, int fp32, Raw &r) {
+template <bool VEC>
+__device__ __forceinline__ void load8(const void *p, int64_t base, const Place<VEC> &a, int i, int fp32, Raw &r) {
     const int64_t at = base + a.at(i);
-    if (a.whole(i)) {
+    if constexpr (VEC) {
         if (fp32) {
             asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                          : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]),
@@ -127,17 +112,16 @@ __device__ __forceinline__ void load8(const void *p, int64_t base, const Place<A
         load_singles(static_cast<const uint32_t *>(p) + at, a, i, r);
     } else {
         load_singles(static_cast<const uint16_t *>(p) + at, a, i, r);
-        if constexpr (kPairs<A>) pack_pairs(r);
     }
 }
 
-template <bool PAIRS>
+template <bool VEC>
 __device__ __forceinline__ void unpack8(const Raw &r, int fp32, float2 (&f)[4]) {
     if (fp32) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             f[k] = make_float2(__uint_as_float(r.w[2 * k]), __uint_as_float(r.w[2 * k + 1]));
-    } else if constexpr (PAIRS) {
+    } else if constexpr (VEC) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             f[k] = make_float2(__uint_as_float(r.w[k] << 16), __uint_as_float(r.w[k] & 0xFFFF0000u));
@@ -148,36 +132,25 @@ __device__ __forceinline__ void unpack8(const Raw &r, int fp32, float2 (&f)[4]) 
     }
 }
 
-// chunk i of a weight, bias or gate row: as load8, but in shifted rows their
-// own starts are elsewhere, so 8 reads of neighbouring values (from L1)
-template <Access A>
-__device__ __forceinline__ void load8_weights(const void *p, int64_t base, const Place<A> &a, int i, int fp32, Raw &r) {
-    if constexpr (A != kShifted) {
-        load8(p, base, a, i, fp32, r);
-    } else {
-        const int64_t at = base + a.at(i);
-        const uint32_t *q = static_cast<const uint32_t *>(p) + at;
-        const uint16_t *h = static_cast<const uint16_t *>(p) + at;
-        if (a.whole(i)) {
+template <class T, class Convert>
+__device__ __forceinline__ void store_singles(T *q, const Place<false> &a, int i, const float2 (&f)[4],
+                                              const Convert &convert) {
+    auto value = [&](int k) { return convert(k & 1 ? f[k / 2].y : f[k / 2].x); };
+    if (a.full(i)) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) r.w[k] = fp32 ? q[k] : h[k];
-        } else if (fp32) {
-            load_singles(q, a, i, r);
-        } else {
-            load_singles(h, a, i, r);
-        }
+        for (int k = 0; k < 8; ++k) q[k * a.step] = value(k);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (a.in(i, k)) q[k * a.step] = value(k);
     }
 }
-template <Access A>
-__device__ __forceinline__ void unpack8_weights(const Raw &r, int fp32, float2 (&f)[4]) {
-    unpack8<A == kWide>(r, fp32, f);
-}
 
-template <Access A>
-__device__ __forceinline__ void store8(void *p, int64_t base, const Place<A> &a, int i, int fp32,
+template <bool VEC>
+__device__ __forceinline__ void store8(void *p, int64_t base, const Place<VEC> &a, int i, int fp32,
                                        const float2 (&f)[4]) {
     const int64_t at = base + a.at(i);
-    if (a.whole(i)) {
+    if constexpr (VEC) {
         if (fp32) {
             asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float *>(p) + at),
                          "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x),
@@ -192,16 +165,10 @@ __device__ __forceinline__ void store8(void *p, int64_t base, const Place<A> &a,
             }
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+    } else if (fp32) {
+        store_singles(static_cast<float *>(p) + at, a, i, f, [](float v) { return v; });
     } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float v = k & 1 ? f[k / 2].y : f[k / 2].x;
-            if (!a.in(i, k)) continue;
-            if (fp32)
-                static_cast<float *>(p)[at + k * a.step()] = v;
-            else
-                static_cast<__nv_bfloat16 *>(p)[at + k * a.step()] = __float2bfloat16_rn(v);
-        }
+        store_singles(static_cast<__nv_bfloat16 *>(p) + at, a, i, f, [](float v) { return __float2bfloat16_rn(v); });
     }
 }
 
@@ -242,8 +209,8 @@ struct Team {
 
 // The row normed in place, times `scale`.  Values behind the row are zero
 // before and after.
-template <class TY, int NV, Access A>
-__device__ __forceinline__ void norm_row(const NormSpec &n, float scale, const Place<A> &at, Team &team,
+template <class TY, int NV, bool VEC>
+__device__ __forceinline__ void norm_row(const NormSpec &n, float scale, const Place<VEC> &at, Team &team,
                                          float2 (&v)[NV][4]) {
     const float inv_c = 1.0f / static_cast<float>(at.C);
     const int fp32 = TY::weight(n);
@@ -256,7 +223,7 @@ __device__ __forceinline__ void norm_row(const NormSpec &n, float scale, const P
         const float mean = team.sum(s.x + s.y) * inv_c;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (at.whole(i) && at.has(i)) {
+            if (at.full(i)) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i][k] = add2(v[i][k], both(-mean));
             } else {
@@ -268,14 +235,12 @@ __device__ __forceinline__ void norm_row(const NormSpec &n, float scale, const P
             }
         }
     }
-    // the weights are on their way during the reduction (shifted rows: 8 words
-    // a chunk, so where four chunks leave no registers they are read when used)
-    constexpr bool kEarly = A != kShifted || NV < 4;
+    // the weights are on their way during the reduction
     Raw w[NV];
-    if (kEarly && n.weight) {
+    if (n.weight) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (at.has(i)) load8_weights(n.weight, 0, at, i, fp32, w[i]);
+            if (at.has(i)) load8(n.weight, 0, at, i, fp32, w[i]);
     }
     float2 s = both(0.0f);
 #pragma unroll
@@ -290,15 +255,14 @@ __device__ __forceinline__ void norm_row(const NormSpec &n, float scale, const P
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[i][k] = mul2(v[i][k], both(inv));
         if (n.weight) {
-            if (!kEarly) load8_weights(n.weight, 0, at, i, fp32, w[i]);
-            unpack8_weights<A>(w[i], fp32, f);
+            unpack8<VEC>(w[i], fp32, f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i][k] = mul2(v[i][k], f[k]);
         }
         if (n.bias) {
             Raw b;
-            load8_weights(n.bias, 0, at, i, fp32, b);
-            unpack8_weights<A>(b, fp32, f);
+            load8(n.bias, 0, at, i, fp32, b);
+            unpack8<VEC>(b, fp32, f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i][k] = fma2(both(scale), f[k], v[i][k]);
         }
@@ -310,8 +274,8 @@ __device__ __forceinline__ void norm_row(const NormSpec &n, float scale, const P
 // correctly rounded z / s (P. Markstein, "Computation of elementary functions
 // on the IBM RISC System/6000 processor", 1990) wherever nothing underflows;
 // scales outside 2^-60 .. 2^60 take the division.
-template <int NV, Access A>
-__device__ __forceinline__ void store_codes(const BlockNormParams &p, int64_t m, const Place<A> &at, Team &team,
+template <int NV, bool VEC>
+__device__ __forceinline__ void store_codes(const BlockNormParams &p, int64_t m, const Place<VEC> &at, Team &team,
                                             const float2 (&v)[NV][4]) {
     float amax = 0.0f;  // values behind the row are zero
 #pragma unroll
@@ -337,19 +301,19 @@ __device__ __forceinline__ void store_codes(const BlockNormParams &p, int64_t m,
                 q = fma2(fma2(q, both(-s), v[i][k]), both(r), q);
             c[k] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
         }
-        if (at.whole(i)) {
+        if constexpr (VEC) {
             *reinterpret_cast<uint2 *>(z + at.at(i)) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (at.in(i, k)) z[at.at(i) + k * at.step()] = static_cast<uint8_t>(c[k / 2] >> (8 * (k & 1)));
+                if (at.in(i, k)) z[at.at(i) + k * at.step] = static_cast<uint8_t>(c[k / 2] >> (8 * (k & 1)));
         }
     }
 }
 
 // From the branch's values to the stores; `res(i, f)` gives the residual's chunk i.
-template <class TY, int NV, Access A, class Res>
-__device__ __forceinline__ void finish_row(const BlockNormParams &p, int64_t m, const Place<A> &at, Team &team,
+template <class TY, int NV, bool VEC, class Res>
+__device__ __forceinline__ void finish_row(const BlockNormParams &p, int64_t m, const Place<VEC> &at, Team &team,
                                            float2 (&v)[NV][4], const Res &res) {
     // the scale rides on the post norm's factor, or on the sum with the residual
     const float scale = p.post.kind == kNormNone ? p.scale : 1.0f;
@@ -362,8 +326,8 @@ __device__ __forceinline__ void finish_row(const BlockNormParams &p, int64_t m, 
         float2 f[4];
         if (p.gate) {
             Raw g;
-            load8_weights(p.gate, g0, at, i, TY::gate(p), g);
-            unpack8_weights<A>(g, TY::gate(p), f);
+            load8(p.gate, g0, at, i, TY::gate(p), g);
+            unpack8<VEC>(g, TY::gate(p), f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i][k] = mul2(v[i][k], f[k]);
         }
@@ -388,7 +352,7 @@ __device__ __forceinline__ void finish_row(const BlockNormParams &p, int64_t m, 
     }
 }
 
-template <class TY, int NV, int MAXT, int MINB, bool PREFETCH, Access A>
+template <class TY, int NV, int MAXT, int MINB, bool PREFETCH, bool VEC>
 __global__ void __launch_bounds__(MAXT, MINB)
 block_norm_kernel(const __grid_constant__ BlockNormParams p, int threads) {
     __shared__ __align__(16) float red[64];
@@ -402,7 +366,7 @@ block_norm_kernel(const __grid_constant__ BlockNormParams p, int threads) {
     const int64_t m = static_cast<int64_t>(blockIdx.x) * (blockDim.x / threads) + threadIdx.x / threads;
     if (m >= p.M) return;  // whole warps: several rows to the block only where a row is one warp
     Team team{red, threads, t, 1};  // a row of several warps is alone in its block
-    const Place<A> at{t, threads, p.C, (p.phase0 + static_cast<int>(m & 7) * p.phase_step) & 7};
+    const Place<VEC> at{t, threads, p.C};
 
     const int64_t r0 = m * p.residual_stride;
     Raw res[NV];
@@ -420,7 +384,7 @@ block_norm_kernel(const __grid_constant__ BlockNormParams p, int threads) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (at.has(i)) {
-                unpack8<kPairs<A>>(raw[i], TY::branch(p), v[i]);
+                unpack8<VEC>(raw[i], TY::branch(p), v[i]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i][k] = both(0.0f);
@@ -429,7 +393,7 @@ block_norm_kernel(const __grid_constant__ BlockNormParams p, int threads) {
     }
     finish_row<TY>(p, m, at, team, v, [&](int i, float2(&f)[4]) {
         if (!PREFETCH) load8(p.residual, r0, at, i, TY::residual(p), res[i]);
-        unpack8<kPairs<A>>(res[i], TY::residual(p), f);
+        unpack8<VEC>(res[i], TY::residual(p), f);
     });
 }
 
@@ -467,7 +431,7 @@ block_norm_stream_kernel(const __grid_constant__ BlockNormParams p, int threads)
 
     const int teams = blockDim.x / threads, j = threadIdx.x / threads, t = threadIdx.x % threads;
     Team team{red + 64 * j, threads, t, 1 + j};
-    const Place<kWide> at{t, threads, C, 0};
+    const Place<true> at{t, threads, C};
     const int plane = NV * threads;
     const int bp = TY::branch(p) ? 2 : 1, rp = p.residual ? (TY::residual(p) ? 2 : 1) : 0;
     const int slot_stride = teams * (bp + rp) * plane;
@@ -588,10 +552,9 @@ block_norm_stream_kernel(const __grid_constant__ BlockNormParams p, int threads)
     copies_left<0>();
 }
 
-template <class TY, int NV, int MAXT, int MINB, bool PREFETCH, Access A>
+template <class TY, int NV, int MAXT, int MINB, bool PREFETCH, bool VEC>
 cudaError_t run_types(const BlockNormParams &p, cudaStream_t stream) {
-    const int width = p.C + (A == kShifted ? 7 : 0);
-    const int threads = ((width + 8 * NV - 1) / (8 * NV) + 31) / 32 * 32;
+    const int threads = ((p.C + 8 * NV - 1) / (8 * NV) + 31) / 32 * 32;
     if (threads > MAXT) return cudaErrorInvalidValue;
     const int rows = threads == 32 ? 4 : 1;  // rows to the block
     cudaLaunchConfig_t cfg = {};
@@ -603,24 +566,17 @@ cudaError_t run_types(const BlockNormParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, block_norm_kernel<TY, NV, MAXT, MINB, PREFETCH, A>, p, threads);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, block_norm_kernel<TY, NV, MAXT, MINB, PREFETCH, VEC>, p, threads);
     if (err == cudaSuccess) note_launches(1);
     return err;
 }
 
 template <int NV, int MAXT, int MINB, bool PREFETCH>
-cudaError_t run(const BlockNormParams &p, Access access, cudaStream_t stream) {
-    if (access == kSingle) return run_types<AnyTypes, NV, MAXT, MINB, PREFETCH, kSingle>(p, stream);
-    // four chunks of shifted rows do not fit 64 registers
-    constexpr int B = NV == 4 ? 1 : MINB;
-    if (AllBf16::fit(p))
-        return access == kWide ? run_types<AllBf16, NV, MAXT, MINB, PREFETCH, kWide>(p, stream)
-                               : run_types<AllBf16, NV, MAXT, B, PREFETCH, kShifted>(p, stream);
-    if (Fp32Stream::fit(p))
-        return access == kWide ? run_types<Fp32Stream, NV, MAXT, MINB, PREFETCH, kWide>(p, stream)
-                               : run_types<Fp32Stream, NV, MAXT, B, PREFETCH, kShifted>(p, stream);
-    return access == kWide ? run_types<AnyTypes, NV, MAXT, MINB, PREFETCH, kWide>(p, stream)
-                           : run_types<AnyTypes, NV, MAXT, B, PREFETCH, kShifted>(p, stream);
+cudaError_t run(const BlockNormParams &p, bool vec, cudaStream_t stream) {
+    if (!vec) return run_types<AnyTypes, NV, MAXT, MINB, PREFETCH, false>(p, stream);
+    if (AllBf16::fit(p)) return run_types<AllBf16, NV, MAXT, MINB, PREFETCH, true>(p, stream);
+    if (Fp32Stream::fit(p)) return run_types<Fp32Stream, NV, MAXT, MINB, PREFETCH, true>(p, stream);
+    return run_types<AnyTypes, NV, MAXT, MINB, PREFETCH, true>(p, stream);
 }
 
 constexpr int kNormSmem = 216 * 1024;
@@ -670,8 +626,7 @@ bool rows_aligned(const void *p, int64_t stride, int elem, int align) {
 
 }  // namespace
 
-cudaError_t launch_block_norm(const BlockNormParams &call, cudaStream_t stream) {
-    BlockNormParams p = call;
+cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream) {
     // bf16 chunks are accessed as 16 bytes, fp32 ones as 32, codes as 8
     auto fits = [](const void *q, int64_t stride, int fp32) {
         return rows_aligned(q, stride, fp32 ? 4 : 2, fp32 ? 32 : 16);
@@ -681,32 +636,6 @@ cudaError_t launch_block_norm(const BlockNormParams &call, cudaStream_t stream) 
                fits(p.h, p.h_stride, p.h_fp32) &&
                (p.z_type == kZE4m3 ? rows_aligned(p.z, p.z_stride, 1, 8) : fits(p.z, p.z_stride, p.z_type == kZFp32));
     for (const NormSpec *n : {&p.post, &p.pre}) vec = vec && fits(n->weight, 0, n->fp32) && fits(n->bias, 0, n->fp32);
-    Access access = vec ? kWide : kSingle;
-    // Shifted rows read weights one value at a time from 8 consecutive ones a
-    // thread, which costs up to 8 times the passes through L1 (most for fp32
-    // weights) and pays where the rows' own traffic weighs more.  Measured (us,
-    // shifted / single): bf16 and one weight 777x1001 4.7 / 5.5, 1541x8585 33.9 /
-    // 51.6, 300x30001 26.4 / 48.6, but 20000x333 24.3 / 23.1; fp32 branch,
-    // two norms with bf16 weights 3000x1001 15.3 / 13.9, 4096x4100 69 / 83;
-    // two fp32 weights 300x5247 14.2 / 11.4, 1541x8585 59 / 70; three
-    // 4096x4100 127 / 97, 1000x13491 113 / 93.
-    int fp32_weights = p.gate && p.gate_fp32;
-    for (const NormSpec *n : {&p.post, &p.pre}) fp32_weights += n->fp32 * ((n->weight ? 1 : 0) + (n->bias ? 1 : 0));
-    const int from = fp32_weights > 2 ? kNormMaxC : fp32_weights ? 8192 : p.branch_fp32 ? 4096 : 512;
-    if (!vec && p.C > from && p.C + 7 <= kNormMaxC) {
-        // whether every tensor of M rows starts each of them at the same place
-        // between two 8-element boundaries (contiguous rows of any C do)
-        auto phase = [](const void *q, int elem) { return static_cast<int>(reinterpret_cast<uintptr_t>(q) / elem % 8); };
-        p.phase0 = phase(p.branch, p.branch_fp32 ? 4 : 2);
-        p.phase_step = static_cast<int>(p.branch_stride % 8);
-        auto same = [&](const void *q, int64_t stride, int elem) {
-            return !q || (phase(q, elem) == p.phase0 && stride % 8 == p.phase_step);
-        };
-        if (same(p.residual, p.residual_stride, p.residual_fp32 ? 4 : 2) && same(p.h, p.h_stride, p.h_fp32 ? 4 : 2) &&
-            same(p.z, p.z_stride, p.z_type == kZE4m3 ? 1 : p.z_type == kZFp32 ? 4 : 2))
-            access = kShifted;
-    }
-    const int width = p.C + (access == kShifted ? 7 : 0);
     const int64_t values = p.M * p.C;
     // Measured on B200, calls in a graph over inputs beyond L2, us a call:
     // - few rows: one chunk a thread, a row's chain of loads, reductions and
@@ -725,10 +654,10 @@ cudaError_t launch_block_norm(const BlockNormParams &call, cudaStream_t stream) 
             return run_stream<4, 768>(p, stream);
         if (stream_teams<2, 1024>(p, &threads, &smem) > 0) return run_stream<2, 1024>(p, stream);
     }
-    if (width > 16384) return run<4, 1024, 1, false>(p, access, stream);
-    if (width <= 256 || (width <= 8192 && values <= 1500000)) return run<1, 1024, 1, true>(p, access, stream);
-    if (width <= 512 || (width <= 8192 && values < 8000000)) return run<2, 512, 1, true>(p, access, stream);
-    return run<4, 512, 2, false>(p, access, stream);
+    if (p.C > 16384) return run<4, 1024, 1, false>(p, vec, stream);
+    if (p.C <= 256 || (p.C <= 8192 && values <= 1500000)) return run<1, 1024, 1, true>(p, vec, stream);
+    if (p.C <= 512 || (p.C <= 8192 && values < 8000000)) return run<2, 512, 1, true>(p, vec, stream);
+    return run<4, 512, 2, false>(p, vec, stream);
 }
 
 }  // namespace patchk

@@ -345,7 +345,6 @@ struct BlockNormParams {
     float scale;
     int C, branch_fp32, residual_fp32, gate_fp32, h_fp32, z_type;
     int num_sms;
-    int phase0 = 0, phase_step = 0;  // rows' starts within chunks of 8 elements (csrc/block_norm.cu)
 };
 cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream);
 
