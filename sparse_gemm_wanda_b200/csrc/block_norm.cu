@@ -655,8 +655,21 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream) {
         if (stream_teams<2, 1024>(p, &threads, &smem) > 0) return run_stream<2, 1024>(p, stream);
     }
     if (p.C > 16384) return run<4, 1024, 1, false>(p, vec, stream);
-    if (p.C <= 256 || (p.C <= 8192 && values <= 1500000)) return run<1, 1024, 1, true>(p, vec, stream);
-    if (p.C <= 512 || (p.C <= 8192 && values < 8000000)) return run<2, 512, 1, true>(p, vec, stream);
+    // Where types are known at run time only (and where accesses are single),
+    // two chunks at most: the conversions leave no registers for four (4096 x
+    // 4096, fp32 weights, a layer norm 31.6 against 40.8, two with a gate 46.7
+    // against 59.8, fp32 rows 39.6 against 52.9), and wide ones are worth it
+    // earlier (300 x 4096 4.4 against 5.4).
+    const bool any = !vec || !(AllBf16::fit(p) || Fp32Stream::fit(p));
+    const int64_t one = any && vec ? 500000 : 1500000, two = any ? 2000000 : 8000000;
+    if (p.C <= 256 || (p.C <= 8192 && values <= one)) return run<1, 1024, 1, true>(p, vec, stream);
+    if (p.C <= 8192 && (p.C <= 512 || values < two)) return run<2, 512, 1, true>(p, vec, stream);
+    if (any && p.C <= 8192)
+        return vec ? run_types<AnyTypes, 2, 512, 2, true, true>(p, stream)
+                   : run_types<AnyTypes, 2, 512, 2, true, false>(p, stream);
+    // (1500 x 12000, a layer norm, 48.2 against 59.3; single accesses, whose
+    // 1541 x 8585 takes 46.6 this way, keep four: 37.7)
+    if (any && vec) return run_types<AnyTypes, 2, 1024, 1, true, true>(p, stream);
     return run<4, 512, 2, false>(p, vec, stream);
 }
 
