@@ -68,6 +68,7 @@ struct F8Params {
     int y_fp32;
     uint32_t *status;
     Epilogue epi;
+    int chain;  // kChainLead / kChainFollow, with an epilogue only
 };
 
 // Work item w: tile w / ksplit, k-steps [c0, c1) of it.
@@ -118,8 +119,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int cta = blockIdx.x, P = gridDim.x;
 
+    const int chain = EPI ? p.chain : 0;
     if (threadIdx.x == 0) {
-        pdl_trigger();  // the fix-up (or the next kernel) may start its prologue
+        if (!(chain & kChainLead)) pdl_trigger();  // the fix-up (or the next kernel) may start its prologue
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 2);  // the weight and X producers
             mbar_init(&empty[s], 1);
@@ -142,11 +144,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const bool skip = *abort_flag != 0;
+    if (chain && threadIdx.x == 64) {  // an epilogue thread, which waits here in any case
+        pdl_wait();
+        if (chain & kChainLead) pdl_trigger();
+    }
 
     if (warp == 0) {
         if (lane == 0 && !skip) {
             // ------------------------------------------------------ producer
-            pdl_wait();  // launched as a programmatic dependent: global memory after the wait
+            // launched as a programmatic dependent: global memory after the wait
+            // (a follower starts after the wait of the product before it)
+            if (!(chain & kChainFollow)) pdl_wait();
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
@@ -185,7 +193,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     } else if (warp == 6) {
         if (lane == 0 && !skip) {
             // ---------------------------------------------------- X producer
-            pdl_wait();  // the codes are written by the kernel just before
+            if (!(chain & kChainFollow)) pdl_wait();  // the codes are written by the kernel just before
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
@@ -472,6 +480,7 @@ cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     p.y_fp32 = g.y_fp32;
     p.status = g.status;
     p.epi = g.epi;
+    p.chain = g.chain;
     split_tiles(g, p.tiles, p.steps, &p.ksplit, &p.kper);
     p.items = p.tiles * p.ksplit;
     p.partial = nullptr;
@@ -596,8 +605,19 @@ bool takes_duo_fp8_gated(const Fp8Launch *gs) {
     return dp.bn > 0 && duo_fp8_us(g, dp, 2) <= fp8_us(gs[0]) + fp8_us(gs[1]);
 }
 
+bool fp8_chains(const Fp8Launch &g) {
+    if (!g.epi_on || takes_duo_fp8(g)) return false;
+    const int bn = g.M <= 64 ? 64 : g.M <= 128 ? 128 : 240;
+    const int64_t tiles = (g.N / kBand) * ((g.M + bn - 1) / bn);
+    if (tiles > g.num_sms) return true;
+    int ksplit, kper;
+    split_tiles(g, static_cast<int>(tiles), static_cast<int>(g.K / kF8Step), &ksplit, &kper);
+    return ksplit == 1;
+}
+
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream) {
     if (g.K % kF8Step != 0 || g.N % kBand != 0 || g.M < 1) return cudaErrorInvalidValue;
+    if (g.chain && !fp8_chains(g)) return cudaErrorInvalidValue;
     if (takes_duo_fp8(g)) {
         const DuoFp8Plan dp = plan_duo_fp8(g.N, g.M, g.num_sms, g.all_sparse != 0);
         if (dp.bn > 0) return launch_duo_fp8(g, dp, stream);

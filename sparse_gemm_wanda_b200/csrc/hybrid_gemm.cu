@@ -122,6 +122,7 @@ struct GemmParams {
     int stall_first_kstep;  // failure-detection test hook: CTA 0 never loads its first k-step
     int32_t u0[kMaxStreamKCtas + 1];  // stream-K: first unit of every CTA (u0[P] = units)
     Epilogue epi;
+    int chain;  // kChainLead / kChainFollow, with an epilogue only
 };
 
 // One piece of work of a CTA: k-steps [ks0, ks1) of tile (band, ttile).
@@ -258,12 +259,13 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     // thread 0 (the producer) knows whether it has passed griddepcontrol.wait
     bool waited = true;
 
+    const int chain = EPI ? p.chain : 0;
     if (threadIdx.x == 0) {
-        pdl_trigger();
+        if (!(chain & kChainLead)) pdl_trigger();
         // the packed weights and table are final once the ready flag is seen;
         // otherwise (the packer may be the kernel just before) wait first
         if (ld_acquire_gpu(p.ready) == 0u) pdl_wait();
-        else waited = false;
+        else waited = chain & kChainFollow;  // X is complete when a follower starts
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -303,6 +305,10 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const bool skip = *abort_flag != 0;
+    if (chain && threadIdx.x == 64) {  // an epilogue thread, which waits here in any case
+        pdl_wait();
+        if (chain & kChainLead) pdl_trigger();
+    }
 
     if (warp == 0) {
         if (lane == 0 && !skip) {
@@ -782,6 +788,7 @@ cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) 
     p.ready = g.ready;
     p.stall_first_kstep = g.stall_first_kstep;
     p.epi = g.epi;
+    p.chain = g.chain;
     const int64_t tiles = static_cast<int64_t>(p.bands) * p.ttiles;
     const int64_t slots = static_cast<int64_t>(g.num_sms) * ctas_per_sm;
     // whole tiles when there are at least two waves of them, stream-K otherwise
@@ -909,7 +916,21 @@ Choice choose_kernel(const GemmLaunch &g) {
 
 }  // namespace
 
+bool hybrid_chains(const GemmLaunch &g) {
+    if (!g.epi_on) return false;
+    // the token tile of the one-band kernel, as launch_hybrid_gemm picks it
+    int bn = 0;
+    if (g.pattern == 4)
+        bn = g.M <= 64 ? 64 : 128;
+    else if (g.M > 16 && g.force_kernel == 1)
+        bn = g.M <= 64 ? 64 : 160;
+    else if (g.M > 16 && g.force_kernel == 0 && !takes_split_k(g.M, g.K, 0))
+        bn = g.M <= 64 ? 64 : choose_kernel(g).kernel != 1 ? 0 : g.M <= 128 ? 128 : 160;
+    return bn && one_band_estimate(g, bn, g.pattern == 4).whole;
+}
+
 cudaError_t launch_hybrid_gemm(const GemmLaunch &g, cudaStream_t stream) {
+    if (g.chain && !hybrid_chains(g)) return cudaErrorInvalidValue;
     if (g.pattern == 4) {
         // 4:8 handles: the one-band kernel with converter warps, every M
         // (stream-K over (tile, k-pair) units when tiles are few)

@@ -991,7 +991,7 @@ static patch_status free_codes(const XCodes &x, cudaError_t e, cudaStream_t stre
 }
 
 static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
-                             int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream) {
+                             int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, int chain) {
     XCodes x;
     cudaError_t e = codes_of(Wp, X, x_scales, M, &x, stream);
     const int force = g_test_kernel.load(std::memory_order_relaxed);
@@ -1001,7 +1001,9 @@ static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float 
         const patchk::GemmLaunch g = fp8_split_launch(Wp, x.q, x.s, M, Y, y_is_fp32, epi);
         e = patchk::launch_decode_f8(&g, 1, stream);
     } else if (e == cudaSuccess) {
-        e = patchk::launch_fp8_gemm(fp8_launch(Wp, x.q, x.s, M, Y, y_is_fp32, epi), stream);
+        patchk::Fp8Launch g = fp8_launch(Wp, x.q, x.s, M, Y, y_is_fp32, epi);
+        g.chain = chain;
+        e = patchk::launch_fp8_gemm(g, stream);
     }
     return free_codes(x, e, stream);
 }
@@ -1045,9 +1047,21 @@ static patchk::GemmLaunch gemm_launch(const patch_packed *Wp, const void *X_bf16
 }
 
 static patch_status product_one(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
-                                int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream) {
-    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, epi, stream);
-    return from_cuda(patchk::launch_hybrid_gemm(gemm_launch(Wp, X, M, Y, y_is_fp32, epi), stream));
+                                int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, int chain = 0) {
+    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, epi, stream, chain);
+    patchk::GemmLaunch g = gemm_launch(Wp, X, M, Y, y_is_fp32, epi);
+    g.chain = chain;
+    return from_cuda(patchk::launch_hybrid_gemm(g, stream));
+}
+
+// whether product_one is one kernel that can lead or follow another (see kChainLead)
+static bool chains(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M,
+                   const patchk::Epilogue *epi) {
+    if (Wp->pattern != 8) return patchk::hybrid_chains(gemm_launch(Wp, X, M, nullptr, 0, epi));
+    // with X already quantised, and not on the split-K kernel
+    if (!x_scales || (M <= patchk::kDecodeMaxM && Wp->dec_nchunks > 0 && g_test_kernel.load(std::memory_order_relaxed) == 0))
+        return false;
+    return patchk::fp8_chains(fp8_launch(Wp, nullptr, nullptr, M, nullptr, 0, epi));
 }
 
 patch_status patch_hybrid_gemm(const patch_packed *Wp, const void *X_bf16, int64_t M, void *Y,
@@ -1150,8 +1164,14 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
             x_scales = x.s;
         }
         patch_status st = PATCH_OK;
-        for (int i = 0; i < count && st == PATCH_OK; ++i)
-            st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream);
+        bool follows = false, next = epis && count > 1 && chains(Wps[0], X, x_scales, M, epi(0));
+        for (int i = 0; i < count && st == PATCH_OK; ++i) {
+            const bool can = next;
+            next = can && i + 1 < count && chains(Wps[i + 1], X, x_scales, M, epi(i + 1));
+            const int chain = follows ? patchk::kChainFollow : next ? patchk::kChainLead : 0;
+            st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream, chain);
+            follows = next;
+        }
         const patch_status st2 = free_codes(x, cudaSuccess, stream);
         return st != PATCH_OK ? st : st2;
     }
@@ -1266,8 +1286,10 @@ static patch_status gated_products(const patch_packed *const *hs, const void *X,
     patchk::Epilogue first = gate, second = up;
     first.ldy = N;
     second.mul = held;
-    patch_status st = product_one(hs[0], X, x_scales, M, held, 1, &first, stream);
-    if (st == PATCH_OK) st = product_one(hs[1], X, x_scales, M, Y, y_is_fp32, &second, stream);
+    const bool both = chains(hs[0], X, x_scales, M, &first) && chains(hs[1], X, x_scales, M, &second);
+    patch_status st = product_one(hs[0], X, x_scales, M, held, 1, &first, stream, both ? patchk::kChainLead : 0);
+    if (st == PATCH_OK)
+        st = product_one(hs[1], X, x_scales, M, Y, y_is_fp32, &second, stream, both ? patchk::kChainFollow : 0);
     const patch_status st2 = free_codes(x, cudaFreeAsync(held, stream), stream);
     return st != PATCH_OK ? st : st2;
 }

@@ -152,7 +152,20 @@ struct GemmLaunch {
     const float *f8_sx;      // [M] token scales
     int epi_on = 0;          // Y takes the epilogue `epi` (else the plain sums, rows of N)
     Epilogue epi;
+    int chain = 0;           // kChainLead / kChainFollow (only where hybrid_chains)
 };
+
+// Products that read the same X, launched one after another as one kernel of
+// whole tiles each, run side by side where the earlier ones leave SMs idle:
+// the first (lead) lets its dependent launch only once its own wait for the
+// stream's earlier work has returned, so X is complete when a follower starts,
+// and a follower reads X at once.  Its epilogue waits for the kernel before it
+// as ever, so the chain is complete when its last kernel is.
+enum { kChainLead = 1, kChainFollow = 2 };
+// whether launch_hybrid_gemm / launch_fp8_gemm run this product as one such kernel
+bool hybrid_chains(const GemmLaunch &g);
+struct Fp8Launch;
+bool fp8_chains(const Fp8Launch &g);
 
 // Picks the configuration (token tile, schedule) for M and launches.
 cudaError_t launch_hybrid_gemm(const GemmLaunch &g, cudaStream_t stream);
@@ -293,6 +306,7 @@ struct Fp8Launch {
     cudaMemPool_t pool;      // split-K partials of the one-band kernel (null: no split)
     int epi_on = 0;          // as GemmLaunch
     Epilogue epi;
+    int chain = 0;
 };
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream);
 // whether launch_fp8_gemm runs the two-SM kernel for this product

@@ -827,3 +827,53 @@ def test_norm_wide_rows_between_boundaries_in_place(P, gen, C, step):
         for i in (1, 2):
             keep[i][shifts[i]: shifts[i] + M * step].view(M, step)[:, :C] = view[i]
             assert torch.equal(big[i], keep[i])
+
+
+@pytest.mark.parametrize("kind", ["2:4", "4:8", "fp8"])
+@pytest.mark.parametrize("M", [20, 100, 300])
+def test_members_side_by_side_read_a_finished_input(P, gen, kind, M):
+    # products that run one after another as single kernels may overlap: each
+    # reads the X that the kernel before the group has just written
+    ws = [Weight(P, gen, n, 640, kind) for n in (384, 128, 384)]
+    packed = [w.packed for w in ws]
+    rows = [randn(gen, M, 640, dtype=BF) for _ in range(2)]
+    z = torch.empty(M, 640, dtype=torch.uint8 if kind == "fp8" else BF, device="cuda")
+    res = randn(gen, M, 384, dtype=BF)
+
+    def step(i):
+        n = P.patch_block_norm(rows[i], pre=("layer", None, None, 1e-5), z_type="e4m3" if kind == "fp8" else "bf16",
+                               want_h=False, out_z=z)
+        ys = P.patch_hybrid_linear_group(packed, z, x_scales=n["scales"], activation="silu", residuals=[res, None, res])
+        g = P.patch_hybrid_gated(packed[0], packed[2], z, x_scales=n["scales"])
+        # reads the group's outputs at once
+        return *ys, g, P.patch_block_norm(g, residual=ys[2], want_h=True)["h"], n["scales"]
+
+    want = []
+    for i in range(2):
+        n = P.patch_block_norm(rows[i], pre=("layer", None, None, 1e-5), z_type="e4m3" if kind == "fp8" else "bf16",
+                               want_h=False)
+        torch.cuda.synchronize()
+        one = []
+        for p, r in zip(packed, (res, None, res)):
+            one.append(P.patch_hybrid_linear(p, n["z"], x_scales=n["scales"], activation="silu", residual=r))
+            torch.cuda.synchronize()
+        want.append((n, one))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(0)
+    for k in range(30):
+        graph.replay()
+        got = [step(1), step(0), step(1)]
+        torch.cuda.synchronize()
+        for i, g in ((0, captured), (1, got[0]), (0, got[1]), (1, got[2])):
+            n, one = want[i]
+            for y, y1, w, r in zip(g, one, ws, (res, None, res)):
+                if M > 64:  # one kernel either way
+                    assert torch.equal(y, y1)
+                elif k == 0:
+                    check_linear(y, w, n["z"], n["scales"], act="silu", residual=r)
+            if k == 0:
+                check_gated(g[3], ws[0], ws[2], n["z"], n["scales"])
+            h = g[3].double() + g[2].double()
+            assert ((g[4].double() - h).abs() <= 2.0 ** -8 * h.abs() + 1e-6).all()
