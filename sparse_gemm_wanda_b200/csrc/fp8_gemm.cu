@@ -144,7 +144,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const bool skip = *abort_flag != 0;
-    if (chain && threadIdx.x == 64) {  // an epilogue thread, which waits here in any case
+    if (threadIdx.x == 64 && ((chain & kChainLead) || (chain && skip))) {  // an epilogue thread
         pdl_wait();
         if (chain & kChainLead) pdl_trigger();
     }
@@ -279,7 +279,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         }
     } else if (!skip) {
         // ------------------------------------------------------- epilogue
-        pdl_wait();  // Y and the partial slots may still be used by earlier kernels
+        // Y and the partial slots may still be used by earlier kernels
+        const bool late = (chain & kChainFollow) && p.ksplit == 1 && !p.epi.mul;
+        if (!late) pdl_wait();
         const int quad = warp % 4;
         const int c_first = EPI && warp >= 7 ? 16 : 0;  // the second group's first chunk
         constexpr int kChunkStep = EPI ? 32 : 16;
@@ -349,6 +351,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
+        if (late) pdl_wait();  // done only when the product before is
     }
     tc_fence_before();
     __syncthreads();
@@ -605,15 +608,7 @@ bool takes_duo_fp8_gated(const Fp8Launch *gs) {
     return dp.bn > 0 && duo_fp8_us(g, dp, 2) <= fp8_us(gs[0]) + fp8_us(gs[1]);
 }
 
-bool fp8_chains(const Fp8Launch &g) {
-    if (!g.epi_on || takes_duo_fp8(g)) return false;
-    const int bn = g.M <= 64 ? 64 : g.M <= 128 ? 128 : 240;
-    const int64_t tiles = (g.N / kBand) * ((g.M + bn - 1) / bn);
-    if (tiles > g.num_sms) return true;
-    int ksplit, kper;
-    split_tiles(g, static_cast<int>(tiles), static_cast<int>(g.K / kF8Step), &ksplit, &kper);
-    return ksplit == 1;
-}
+bool fp8_chains(const Fp8Launch &g) { return g.epi_on && !takes_duo_fp8(g); }
 
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream) {
     if (g.K % kF8Step != 0 || g.N % kBand != 0 || g.M < 1) return cudaErrorInvalidValue;

@@ -305,7 +305,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const bool skip = *abort_flag != 0;
-    if (chain && threadIdx.x == 64) {  // an epilogue thread, which waits here in any case
+    if (threadIdx.x == 64 && ((chain & kChainLead) || (chain && skip))) {  // an epilogue thread
         pdl_wait();
         if (chain & kChainLead) pdl_trigger();
     }
@@ -533,7 +533,9 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         }
     } else if (!skip) {
         // ------------------------------------------------------- epilogue
-        pdl_wait();  // Y and the partials may still be in use by earlier kernels
+        // Y and the partials may still be in use by earlier kernels
+        const bool late = (chain & kChainFollow) && !p.stream_k && !p.epi.mul;
+        if (!late) pdl_wait();
         const int quad = warp % 4;  // TMEM lanes 32*quad .. 32*quad+31
         const int c_first = EPI && warp >= 6 ? 16 : 0;  // the second group's first chunk
         constexpr int kChunkStep = EPI ? 32 : 16;
@@ -595,6 +597,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
+        if (late) pdl_wait();  // done only when the product before is
     }
     tc_fence_before();
     __syncthreads();
@@ -916,17 +919,12 @@ Choice choose_kernel(const GemmLaunch &g) {
 
 }  // namespace
 
-bool hybrid_chains(const GemmLaunch &g) {
+bool hybrid_chains(const GemmLaunch &g) {  // as launch_hybrid_gemm picks the kernel
     if (!g.epi_on) return false;
-    // the token tile of the one-band kernel, as launch_hybrid_gemm picks it
-    int bn = 0;
-    if (g.pattern == 4)
-        bn = g.M <= 64 ? 64 : 128;
-    else if (g.M > 16 && g.force_kernel == 1)
-        bn = g.M <= 64 ? 64 : 160;
-    else if (g.M > 16 && g.force_kernel == 0 && !takes_split_k(g.M, g.K, 0))
-        bn = g.M <= 64 ? 64 : choose_kernel(g).kernel != 1 ? 0 : g.M <= 128 ? 128 : 160;
-    return bn && one_band_estimate(g, bn, g.pattern == 4).whole;
+    if (g.pattern == 4) return true;
+    if (g.M <= 16 || g.force_kernel > 1) return false;
+    if (g.force_kernel == 1) return true;
+    return !takes_split_k(g.M, g.K, 0) && (g.M <= 64 || choose_kernel(g).kernel == 1);
 }
 
 cudaError_t launch_hybrid_gemm(const GemmLaunch &g, cudaStream_t stream) {

@@ -155,14 +155,15 @@ struct GemmLaunch {
     int chain = 0;           // kChainLead / kChainFollow (only where hybrid_chains)
 };
 
-// Products that read the same X, launched one after another as one kernel of
-// whole tiles each, run side by side where the earlier ones leave SMs idle:
-// the first (lead) lets its dependent launch only once its own wait for the
-// stream's earlier work has returned, so X is complete when a follower starts,
-// and a follower reads X at once.  Its epilogue waits for the kernel before it
-// as ever, so the chain is complete when its last kernel is.
+// Products that read the same X, launched one after another on the one-band
+// kernels, run side by side where the earlier ones leave SMs idle: the first
+// (lead) lets its dependent launch only once its own wait for the stream's
+// earlier work has returned, so X, Y and the residual are ready when a follower
+// starts.  A follower reads X at once; its epilogue waits for the kernel before
+// it where it may share memory with that (split ranges' partials, the gate's
+// values), else only at its end, so the chain is complete when its last kernel is.
 enum { kChainLead = 1, kChainFollow = 2 };
-// whether launch_hybrid_gemm / launch_fp8_gemm run this product as one such kernel
+// whether launch_hybrid_gemm / launch_fp8_gemm run this product on such a kernel
 bool hybrid_chains(const GemmLaunch &g);
 struct Fp8Launch;
 bool fp8_chains(const Fp8Launch &g);
