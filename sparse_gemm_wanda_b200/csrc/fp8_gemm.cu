@@ -422,7 +422,7 @@ EncodeTiledFn encode_fn() {
 // two work items fall on every SM (ranges of equal length, none empty); with
 // more tiles the partials and the fix-up cost more than the idle SMs (measured
 // on 11008x4096: 86 tiles, 22.3 us split against 17.3).
-void split_tiles(const Fp8Launch &g, int tiles, int steps, int *ksplit, int *kper) {
+void split_tiles(const Fp8Launch &g, int tiles, int steps, int peers, int *ksplit, int *kper) {
     *ksplit = 1;
     *kper = steps;
     if (2 * tiles <= g.num_sms && g.pool) {
@@ -443,7 +443,9 @@ void split_tiles(const Fp8Launch &g, int tiles, int steps, int *ksplit, int *kpe
     const int rounds = (tiles * *ksplit + g.num_sms - 1) / g.num_sms;
     const double whole = 3.0 + 0.03 * cols + 0.31 * steps;
     const double split = 4.4 + 0.009 * cols + 0.3 * *kper + 1.6 * (rounds - 1) + mn * (8.5 + 0.67 * *ksplit);
-    if (whole <= split) {
+    // peers side by side: whole tiles next to each other, splits one by one
+    const int waves = (peers * tiles + g.num_sms - 1) / g.num_sms;
+    if (waves * whole + 2.0 * (peers - 1) <= peers * split) {
         *ksplit = 1;
         *kper = steps;
     }
@@ -484,7 +486,7 @@ cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     p.status = g.status;
     p.epi = g.epi;
     p.chain = g.chain;
-    split_tiles(g, p.tiles, p.steps, &p.ksplit, &p.kper);
+    split_tiles(g, p.tiles, p.steps, g.peers, &p.ksplit, &p.kper);
     p.items = p.tiles * p.ksplit;
     p.partial = nullptr;
     float *ws = nullptr;
@@ -568,7 +570,7 @@ double one_band_fp8_us(const Fp8Launch &g) {
     const int64_t tiles = (g.N / kBand) * ((g.M + bn - 1) / bn);
     if (tiles > 1 << 24) return 1e9;
     int ksplit, kper;
-    split_tiles(g, static_cast<int>(tiles), static_cast<int>(g.K / kF8Step), &ksplit, &kper);
+    split_tiles(g, static_cast<int>(tiles), static_cast<int>(g.K / kF8Step), 1, &ksplit, &kper);
     const int64_t rounds = (tiles * ksplit + g.num_sms - 1) / g.num_sms;
     const double partial_mb = ksplit > 1 ? 4e-6 * static_cast<double>(g.M) * static_cast<double>(g.N) * ksplit : 0.0;
     // unsplit, a tile's own epilogue of bn columns

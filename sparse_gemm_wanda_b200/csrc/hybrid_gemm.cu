@@ -757,14 +757,17 @@ struct OneBand {
     double us;
     bool whole;
 };
-OneBand one_band_estimate(const GemmLaunch &g, int bn, bool nm) {
+// With `peers` products side by side, whole tiles run next to each other and
+// split ranges one product after another.
+OneBand one_band_estimate(const GemmLaunch &g, int bn, bool nm, int peers = 1) {
     const double sms = g.num_sms, pairs = static_cast<double>(g.K / (2 * kStep));
     const double tiles = static_cast<double>((g.N / kBand) * ((g.M + bn - 1) / bn));
-    const double whole = 4.7 + std::ceil(tiles / sms) * ((nm ? 0.97 : 0.5) * pairs + bn * 1.5 / 160);
+    const double whole = 4.7 + std::ceil(peers * tiles / sms) * ((nm ? 0.97 : 0.5) * pairs + bn * 1.5 / 160) +
+                         2.0 * (peers - 1);
     const double sharing = std::min(62.0, std::max(1.0, std::min(sms, tiles * pairs) / tiles));
     const double stream = 9.5 + (nm ? 1.3 : 0.8) * std::ceil(tiles * pairs / sms) +
                           1e-5 * static_cast<double>(g.M) * static_cast<double>(g.N) + 0.065 * sharing;
-    return tiles >= 2 * sms || whole <= stream ? OneBand{whole, true} : OneBand{stream, false};
+    return tiles >= 2 * sms || whole <= peers * stream ? OneBand{whole, true} : OneBand{stream, false};
 }
 
 template <int BN, int STAGES, bool NM, bool EPI>
@@ -796,7 +799,7 @@ cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) 
     const int64_t slots = static_cast<int64_t>(g.num_sms) * ctas_per_sm;
     // whole tiles when there are at least two waves of them, stream-K otherwise
     // (with an epilogue: whole tiles also where they are estimated faster)
-    const bool sk = tiles < 2 * slots && !(EPI && one_band_estimate(g, BN, NM).whole);
+    const bool sk = tiles < 2 * slots && !(EPI && one_band_estimate(g, BN, NM, g.peers).whole);
     p.stream_k = sk ? 1 : 0;
     p.units = tiles * (p.nsteps / 2);
     // stream-K: at most 62 CTAs per tile, so a tile's partials fit the fix-up's slot list

@@ -991,7 +991,7 @@ static patch_status free_codes(const XCodes &x, cudaError_t e, cudaStream_t stre
 }
 
 static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
-                             int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, int chain) {
+                             int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, int chain, int peers) {
     XCodes x;
     cudaError_t e = codes_of(Wp, X, x_scales, M, &x, stream);
     const int force = g_test_kernel.load(std::memory_order_relaxed);
@@ -1003,6 +1003,7 @@ static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float 
     } else if (e == cudaSuccess) {
         patchk::Fp8Launch g = fp8_launch(Wp, x.q, x.s, M, Y, y_is_fp32, epi);
         g.chain = chain;
+        g.peers = peers;
         e = patchk::launch_fp8_gemm(g, stream);
     }
     return free_codes(x, e, stream);
@@ -1047,10 +1048,12 @@ static patchk::GemmLaunch gemm_launch(const patch_packed *Wp, const void *X_bf16
 }
 
 static patch_status product_one(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
-                                int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, int chain = 0) {
-    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, epi, stream, chain);
+                                int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, int chain = 0,
+                                int peers = 1) {
+    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, epi, stream, chain, peers);
     patchk::GemmLaunch g = gemm_launch(Wp, X, M, Y, y_is_fp32, epi);
     g.chain = chain;
+    g.peers = peers;
     return from_cuda(patchk::launch_hybrid_gemm(g, stream));
 }
 
@@ -1164,13 +1167,11 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
             x_scales = x.s;
         }
         patch_status st = PATCH_OK;
-        bool follows = false, next = epis && count > 1 && chains(Wps[0], X, x_scales, M, epi(0));
+        bool side = epis && count > 1;
+        for (int i = 0; i < count && side; ++i) side = chains(Wps[i], X, x_scales, M, epi(i));
         for (int i = 0; i < count && st == PATCH_OK; ++i) {
-            const bool can = next;
-            next = can && i + 1 < count && chains(Wps[i + 1], X, x_scales, M, epi(i + 1));
-            const int chain = follows ? patchk::kChainFollow : next ? patchk::kChainLead : 0;
-            st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream, chain);
-            follows = next;
+            const int chain = !side ? 0 : i ? patchk::kChainFollow : patchk::kChainLead;
+            st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream, chain, side ? count : 1);
         }
         const patch_status st2 = free_codes(x, cudaSuccess, stream);
         return st != PATCH_OK ? st : st2;

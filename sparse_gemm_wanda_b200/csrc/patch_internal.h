@@ -153,6 +153,7 @@ struct GemmLaunch {
     int epi_on = 0;          // Y takes the epilogue `epi` (else the plain sums, rows of N)
     Epilogue epi;
     int chain = 0;           // kChainLead / kChainFollow (only where hybrid_chains)
+    int peers = 1;           // products that run side by side, this one included
 };
 
 // Products that read the same X, launched one after another on the one-band
@@ -307,7 +308,7 @@ struct Fp8Launch {
     cudaMemPool_t pool;      // split-K partials of the one-band kernel (null: no split)
     int epi_on = 0;          // as GemmLaunch
     Epilogue epi;
-    int chain = 0;
+    int chain = 0, peers = 1;
 };
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream);
 // whether launch_fp8_gemm runs the two-SM kernel for this product
