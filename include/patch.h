@@ -521,7 +521,8 @@ patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const fl
  * patch_hybrid_linear for `count` (1..8) handles that read the same X, each
  * with its own Y and epilogue, launched together where
  * patch_hybrid_gemm_group's products are (one split-K launch at decode token
- * counts, one two-SM launch in prefill, one quantisation of X).
+ * counts, one two-SM launch in prefill, one quantisation of X); others run
+ * side by side where the kernels leave SMs idle.
  *   epis   host array of count epilogues, or NULL for none.
  * Every member's arguments are checked before anything is enqueued.  A
  * handle may appear more than once.  The members run in no order: an output
