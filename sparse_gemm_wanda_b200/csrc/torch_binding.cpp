@@ -10,6 +10,7 @@
 // ValueError; a status other than PATCH_OK is returned as an int for the
 // caller to raise.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -89,6 +90,12 @@ const void *rows(const at::Tensor *t, int64_t M, int64_t C, c10::Device dev, con
     return t->const_data_ptr();
 }
 
+// A new tensor, without at::empty's way through the dispatcher (0.3 to 0.5 us of
+// the 5 to 7 that a small call takes on the host).
+at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
+    return at::detail::empty_cuda(sizes, type, dev, std::nullopt);
+}
+
 // The output of a call: the caller's (checked), or a new tensor in `fresh`.
 PyObject *output(PyObject *given, int64_t M, int64_t C, at::ScalarType type, c10::Device dev, const char *name,
                  at::Tensor *fresh, void **ptr, int64_t *step) {
@@ -97,7 +104,7 @@ PyObject *output(PyObject *given, int64_t M, int64_t C, at::ScalarType type, c10
         Py_INCREF(given);
         return given;
     }
-    *fresh = at::empty({M, C}, at::TensorOptions().dtype(type).device(dev));
+    *fresh = empty({M, C}, type, dev);
     *ptr = fresh->mutable_data_ptr();
     *step = C;
     return THPVariable_Wrap(*fresh);
@@ -319,7 +326,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::ScalarType type = p.z_type == PATCH_Z_BF16 ? at::kBFloat16 : p.z_type == PATCH_Z_FP32 ? at::kFloat : at::kByte;
         z = THPObjectPtr(output(a[10], M, C, type, dev, "out_z", &fresh, &p.z, &p.z_stride));
         if (p.z_type == PATCH_Z_E4M3) {
-            at::Tensor s = at::empty({M}, at::TensorOptions().dtype(at::kFloat).device(dev));
+            at::Tensor s = empty({M}, at::kFloat, dev);
             p.z_scales = s.mutable_data_ptr<float>();
             scales = THPObjectPtr(THPVariable_Wrap(s));
         }
