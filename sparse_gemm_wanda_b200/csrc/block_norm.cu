@@ -360,7 +360,11 @@ block_norm_kernel(const __grid_constant__ BlockNormParams p, int threads) {
         if (threadIdx.x < 64) red[threadIdx.x] = 0.0f;
         __syncthreads();
     }
-    if (threadIdx.x == 0) pdl_trigger();
+    // The next kernel starts early where it can be a product of these rows (its
+    // weights then stream meanwhile: 1 x 4096 and the product 9.7 us in place of
+    // 11.4); other widths' next rows start later but side by side sooner
+    // (777x1001, two layer norms, 5.5 in place of 7.1 a call).
+    if (threadIdx.x == 0 && p.C % 128 == 0) pdl_trigger();
     pdl_wait();
     const int t = threadIdx.x % threads;
     const int64_t m = static_cast<int64_t>(blockIdx.x) * (blockDim.x / threads) + threadIdx.x / threads;
@@ -661,9 +665,10 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream) {
     // against 59.8, fp32 rows 39.6 against 52.9), and wide ones are worth it
     // earlier (300 x 4096 4.4 against 5.4).
     const bool any = !vec || !(AllBf16::fit(p) || Fp32Stream::fit(p));
-    // An fp32 stream keeps two (4096 x 4096 33.3 against 34.9, e4m3 34.7 against 36.9).
+    // An fp32 stream keeps two with one norm (4096 x 4096 33.3 against 34.9, e4m3
+    // 34.7 against 36.9; two norms on 4096 x 5120 53 against 49).
     const int64_t one = any && vec ? 500000 : 1500000;
-    const int64_t two = any ? 2000000 : Fp32Stream::fit(p) ? INT64_MAX : 8000000;
+    const int64_t two = any ? 2000000 : Fp32Stream::fit(p) && p.post.kind == kNormNone ? INT64_MAX : 8000000;
     if (p.C <= 256 || (p.C <= 8192 && values <= one)) return run<1, 1024, 1, true>(p, vec, stream);
     if (p.C <= 8192 && (p.C <= 512 || values < two)) return run<2, 512, 1, true>(p, vec, stream);
     if (any && p.C <= 8192)
