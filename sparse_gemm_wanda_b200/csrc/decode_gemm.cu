@@ -128,6 +128,7 @@ struct DecodeParams {
     const uint32_t *ready[kDecMaxGroup];
     float *partial[kDecMaxGroup];  // per matrix: [its chunks][BN][128]
     uint32_t *counter;  // chunks claimed beyond the first 2 * gridDim.x; zero between calls
+    uint32_t last_claim;  // without a fix-up: the claim that ends the call and zeroes the counter
     int stall_first_kstep;  // failure-detection test hook
     uint64_t first_desc[kDecMaxCtas];   // descriptor of chunk c for c < gridDim.x
     uint64_t second_desc[kDecMaxCtas];  // of chunk c + gridDim.x where that exists
@@ -196,9 +197,15 @@ __device__ __forceinline__ bool wait_count_bounded(volatile uint32_t *ctr, uint3
     }
 }
 
-template <int BN, bool F8>
+// DIRECT: up to 16 tokens, bands of one chunk (K <= 512, FP8 1024) and an
+// epilogue: a chunk's sums are the outputs', so they are finished and stored here
+// and no fix-up follows (2304x512, M = 7: 7.0 -> 4.8 us a call, of which the
+// host's second launch was the most).  `out` is then a ReduceParams, else empty.
+struct NoOut {};
+template <int BN, bool F8, bool DIRECT, class Out>
 __global__ void __launch_bounds__(kDecThreads, 1)
-decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ DecodeParams p) {
+decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ DecodeParams p,
+                   const __grid_constant__ Out out) {
     using C = DecCfg<BN>;
     constexpr int kDecStages = C::kStages;
     constexpr int kDecStageBytes = C::kStageBytes;
@@ -332,6 +339,7 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                         tk = atomicAdd(p.counter, 1u);
                     }
                     have_tk = false;
+                    if (DIRECT && tk == p.last_claim) *p.counter = 0u;
                     jnn = 2 * G + static_cast<int>(tk);
                     if (jnn < p.nchunks) {
                         const int mi = dec_mat_of_band(p, jnn / p.cpb);
@@ -524,6 +532,23 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
         for (int ci = 0;; ++ci) {
             const int buf = ci & 1;
+            // what the epilogue reads for this CTA's first two chunks, which are
+            // known before they are multiplied
+            [[maybe_unused]] int mi = 0;
+            [[maybe_unused]] int64_t n = 0;
+            [[maybe_unused]] float bias = 0.0f, sw = 0.0f;
+            [[maybe_unused]] uint32_t add[16];
+            [[maybe_unused]] auto fetch = [&](int chunk) {
+                if constexpr (DIRECT) {
+                    mi = dec_mat_of_band(p, chunk);
+                    n = static_cast<int64_t>(chunk - p.band0[mi]) * kBand + row;
+                    bias = epi_bias(out.epi[mi], n);
+                    if (F8) sw = __ldg(out.f8_sw[mi] + n);
+                    epi_fetch(out.epi[mi], out.N[mi], 0, n, static_cast<int>(p.M), add);
+                }
+            };
+            const int known = static_cast<int>(blockIdx.x) + ci * static_cast<int>(gridDim.x);
+            if (DIRECT && ci < 2 && known < p.nchunks) fetch(known);
             const bool ok = mbar_wait_bounded(&acc_full[buf], (ci >> 1) & 1u, never_flag, kDecWaitLimitNs);
             tc_fence_after();
             if (!ok) {
@@ -534,6 +559,7 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             const int j = acc_chunk[buf];
             if (j < 0) break;
             const uint32_t mask = acc_mask[buf];  // the same for every lane
+            if (DIRECT && ci >= 2) fetch(j);
             // 16 token columns at a time (columns past M are never stored)
 #pragma unroll 1
             for (int c0 = 0; c0 < BN && c0 < p.M; c0 += 16) {
@@ -542,14 +568,25 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 if (mask & 2u) tmem_ld_32x32b_x16(lane_base + (2 * buf + 1) * BN + c0, r1);
                 tmem_ld_wait();
                 if (*abort_flag == 0) {
-                    const int mi = dec_mat_of_band(p, j / p.cpb);
-                    const int64_t lj = j - static_cast<int64_t>(p.band0[mi]) * p.cpb;  // chunk of matrix mi
-                    float *part = p.partial[mi] + (lj * BN + c0) * kBand + row;
+                    float v[16];
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float v = (mask == 3u) ? __fadd_rn(__uint_as_float(r0[q]), __uint_as_float(r1[q]))
-                                                     : __uint_as_float(mask & 1u ? r0[q] : r1[q]);
-                        if (c0 + q < p.M) part[q * kBand] = v;
+                    for (int q = 0; q < 16; ++q)
+                        v[q] = (mask == 3u) ? __fadd_rn(__uint_as_float(r0[q]), __uint_as_float(r1[q]))
+                                            : __uint_as_float(mask & 1u ? r0[q] : r1[q]);
+                    if constexpr (DIRECT) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            v[q] = __fadd_rn(0.0f, v[q]);  // as the fix-up adds it
+                            if (F8 && q < p.M) v[q] = v[q] * sw * __ldg(out.f8_sx + q);
+                        }
+                        epi_store(out.epi[mi], out.Y[mi], out.y_fp32, 0, n, static_cast<int>(p.M), bias, v, add);
+                    } else {
+                        const int pm = dec_mat_of_band(p, j / p.cpb);
+                        const int64_t lj = j - static_cast<int64_t>(p.band0[pm]) * p.cpb;  // chunk of matrix pm
+                        float *part = p.partial[pm] + (lj * BN + c0) * kBand + row;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            if (c0 + q < p.M) part[q * kBand] = v[q];
                     }
                 }
             }
@@ -675,7 +712,9 @@ namespace {
 template <int BN, bool F8>
 cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, bool gated) {
     using C = DecCfg<BN>;
-    const cudaError_t attr_err = allow_smem<decode_gemm_kernel<BN, F8>>(C::kSmemBytes);
+    cudaError_t attr_err = allow_smem<decode_gemm_kernel<BN, F8, false, NoOut>>(C::kSmemBytes);
+    if (BN == 16 && attr_err == cudaSuccess)
+        attr_err = allow_smem<decode_gemm_kernel<16, F8, true, ReduceParams>>(C::kSmemBytes);
     if (attr_err != cudaSuccess) return attr_err;
     if (count < 1 || count > kDecMaxGroup) return cudaErrorInvalidValue;
     const GemmLaunch &g = gs[0];
@@ -766,14 +805,16 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, 
     for (int i = 0; i < count; ++i)
         own = own && gs[i].workspace &&
               decode_workspace_bytes(gs[i].dec_nchunks, BN) <= gs[i].workspace_bytes;
+    const bool direct = BN == 16 && g.epi_on && !gated && g.dec_cpb == 1;
     float *ws = nullptr;
-    if (!own) {
+    if (!own && !direct) {
         const cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws),
                                                       decode_workspace_bytes(p.nchunks, BN), g.pool, stream);
         if (e != cudaSuccess) return e;
     }
     for (int i = 0; i < kDecMaxGroup; ++i)
         p.partial[i] = i >= count ? nullptr
+                       : direct ? nullptr
                        : own ? gs[i].workspace
                              : ws + static_cast<int64_t>(p.band0[i]) * g.dec_cpb * BN * kBand;
 
@@ -787,17 +828,25 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, decode_gemm_kernel<BN, F8>, map, p);
+    r.cpb = p.cpb;
+    r.nmat = p.nmat;
+    r.counter = p.counter;
+    std::copy(std::begin(p.band0), std::end(p.band0), r.band0);
+    std::copy(std::begin(p.partial), std::end(p.partial), r.partial);
+    // a CTA whose second chunk exists claims until it is told there are no more
+    p.last_claim = static_cast<uint32_t>(std::max<int64_t>(0, nchunks - 2 * grid) +
+                                         std::min<int64_t>(grid, nchunks - grid) - 1);
+    if (direct) {
+        const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_gemm_kernel<16, F8, true, ReduceParams>, map, p, r);
+        if (err == cudaSuccess) note_launches(1);
+        return err;
+    }
+    cudaError_t err = cudaLaunchKernelEx(&cfg, decode_gemm_kernel<BN, F8, false, NoOut>, map, p, NoOut{});
     if (err == cudaSuccess) {
         note_launches(1);
         cfg.gridDim = dim3(static_cast<unsigned>(gated ? g.N / kBand : bands), static_cast<unsigned>(g.M));
         cfg.blockDim = dim3(kBand);
         cfg.dynamicSmemBytes = 0;
-        r.cpb = p.cpb;
-        r.nmat = p.nmat;
-        r.counter = p.counter;
-        std::copy(std::begin(p.band0), std::end(p.band0), r.band0);
-        std::copy(std::begin(p.partial), std::end(p.partial), r.partial);
         err = gated      ? cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiGated>, r)
               : g.epi_on ? cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiLinear>, r)
                          : cudaLaunchKernelEx(&cfg, decode_reduce_kernel<BN, F8, kEpiPlain>, r);
@@ -815,7 +864,8 @@ cudaError_t launch_decode(const GemmLaunch *gs, int count, cudaStream_t stream, 
 template <int BN, bool F8>
 static void preload_decode() {
     cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<BN, F8>);
+    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<BN, F8, false, NoOut>);
+    (void)cudaFuncGetAttributes(&a, decode_gemm_kernel<16, F8, true, ReduceParams>);
     (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<BN, F8, kEpiPlain>);
     (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<BN, F8, kEpiLinear>);
     (void)cudaFuncGetAttributes(&a, decode_reduce_kernel<BN, F8, kEpiGated>);

@@ -874,3 +874,26 @@ def test_members_side_by_side_read_a_finished_input(P, gen, kind, M):
                 check_gated(g[3], ws[0], ws[2], n["z"], n["scales"])
             h = g[3].double() + g[2].double()
             assert ((g[4].double() - h).abs() <= 2.0 ** -8 * h.abs() + 1e-6).all()
+
+
+@pytest.mark.parametrize("kind", ["2:4", "fp8"])
+@pytest.mark.parametrize("bands", [1, 149, 200, 297, 700])
+def test_short_k_and_many_bands(P, gen, kind, bands):
+    # bands of one chunk: more of them than blocks, claimed at run time, call after call
+    w = Weight(P, gen, 128 * bands, 256, kind)
+    other = Weight(P, gen, 256, 256, kind)
+    for M in (3, 40):
+        x, _ = x_of(gen, w, M)
+        b, r = randn(gen, w.N), randn(gen, M, w.N, dtype=BF)
+        first = P.patch_hybrid_linear(w.packed, x, bias=b, residual=r, activation="silu")
+        check_linear(first, w, x, bias=b, residual=r, act="silu")
+        for _ in range(3):
+            assert torch.equal(P.patch_hybrid_linear(w.packed, x, bias=b, residual=r, activation="silu"), first)
+            ys = P.patch_hybrid_linear_group([w.packed, other.packed, w.packed], x, biases=[b, None, b], activation="silu",
+                                             residuals=[r, None, r])
+            assert torch.equal(ys[0], first) and torch.equal(ys[2], first)
+            check_linear(ys[1], other, x, act="silu")
+        # the plain product shares the handle's counter
+        plain = P.patch_hybrid_gemm(w.packed, x, out_fp32=True)
+        assert torch.equal(P.patch_hybrid_linear(w.packed, x, out_fp32=True), plain)
+        assert torch.equal(P.patch_hybrid_gemm(w.packed, x, out_fp32=True), plain)
