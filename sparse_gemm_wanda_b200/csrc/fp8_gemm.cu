@@ -23,7 +23,8 @@
 // Roles (224 threads): warp 0 lane 0 weight producer, warp 6 lane 0 X
 // producer (the copies one thread issues are processed largely one after
 // another, so the two streams go through two threads), warp 1 lane 0 MMA
-// (warp 1 also allocates tensor memory), warps 2..5 epilogue.  Every mbarrier
+// (warp 1 also allocates tensor memory), warps 2..5 (with an epilogue also
+// 7..10) the accumulators.  Every mbarrier
 // wait is bounded by %globaltimer; a wait that runs out raises the handle's
 // status.
 #include <cuda.h>

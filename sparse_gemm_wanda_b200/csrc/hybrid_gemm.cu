@@ -22,7 +22,8 @@
 // acquire at device scope), the k-step table and the first STAGES pairs of
 // packed weights are fetched ahead of the wait, so the weight stream of one
 // GEMM overlaps the tail of the kernel before it.  X, Y and the partials are
-// touched only after the wait.
+// touched only after the wait (products that run side by side: kChainLead in
+// patch_internal.h).
 //
 // Roles (192 threads):
 //   * warp 0, one thread: producer.  Per 64-column k-step it reads the table
