@@ -152,17 +152,17 @@ __device__ __forceinline__ void epi_drain(const Epilogue &e, void *Y, int y_fp32
     }
 }
 
-// One piece of a gated item in a two-SM kernel: this thread's output column n
+// One piece of a gated item in a kernel of whole tiles: this thread's output column n
 // (TMEM lane) for the 16-token chunks 16 * grp + 32 j of an accumulator at
 // tensor-memory address `acc`; `sums(c0, v)` reads a chunk's sums.
 //   gate (mi = 0): act(sum + bias), written back in place chunk by chunk (one
-//     copy of the activation code), then held in 128 registers so that the
-//     accumulator is free for the next item while the up projection runs;
+//     copy of the activation code), then held in 16 J registers (J chunks cover
+//     the tile) so that the accumulator is free while the up projection runs;
 //   up (mi = 1): (sum + bias) * the held gate, stored.
-template <class Sums>
+template <int J, class Sums>
 __device__ __forceinline__ void gated_piece(const Epilogue &e, void *Y, int y_fp32, int mi, uint32_t acc, int grp,
                                             int64_t m_base, int m_valid, int64_t n, float bias,
-                                            uint32_t (&held)[8][16], const Sums &sums) {
+                                            uint32_t (&held)[J][16], const Sums &sums) {
     if (mi == 0) {
 #pragma unroll 1
         for (int c0 = 16 * grp; c0 < m_valid; c0 += 32) {
@@ -178,14 +178,14 @@ __device__ __forceinline__ void gated_piece(const Epilogue &e, void *Y, int y_fp
         }
         tmem_st_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < J; ++j)
             if (16 * grp + 32 * j < m_valid)
                 tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(16 * grp + 32 * j), held[j]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) tmem_ld_wait(held[j]);
+        for (int j = 0; j < J; ++j) tmem_ld_wait(held[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < J; ++j) {
             const int c0 = 16 * grp + 32 * j;
             if (c0 < m_valid) {
                 float v[16];

@@ -123,6 +123,12 @@ struct GemmParams {
     int stall_first_kstep;  // failure-detection test hook: CTA 0 never loads its first k-step
     int32_t u0[kMaxStreamKCtas + 1];  // stream-K: first unit of every CTA (u0[P] = units)
     Epilogue epi;
+    // gated pairs: the up projection's (p.packed, .. are the gate's)
+    const uint8_t *up_packed;
+    const uint64_t *up_table;
+    uint32_t *up_status;
+    const uint32_t *up_ready;
+    Epilogue up_epi;
     int chain;  // kChainLead / kChainFollow, with an epilogue only
 };
 
@@ -143,11 +149,14 @@ __device__ __forceinline__ int sk_cta_of(const int32_t *u0, int P, int64_t x) {
     return lo;
 }
 
+// Gated: whole tiles, segment 2q a tile of the gate and 2q + 1 the same tile of
+// the up projection.
+template <bool GATED>
 __device__ __forceinline__ bool get_segment(const GemmParams &p, int c, int i, Segment &s) {
     const int P = gridDim.x;
     const int tiles = p.bands * p.ttiles;
-    if (!p.stream_k) {
-        const int64_t t = static_cast<int64_t>(c) + static_cast<int64_t>(i) * P;
+    if (GATED || !p.stream_k) {
+        const int64_t t = static_cast<int64_t>(c) + static_cast<int64_t>(GATED ? i >> 1 : i) * P;
         if (t >= tiles) return false;
         s.tile = static_cast<int>(t);
         s.ks0 = 0;
@@ -172,6 +181,12 @@ __device__ __forceinline__ bool get_segment(const GemmParams &p, int c, int i, S
     s.band = s.tile / p.ttiles;
     s.ttile = s.tile % p.ttiles;
     return true;
+}
+
+template <bool GATED>
+__device__ __forceinline__ void raise_timeout(const GemmParams &p) {
+    atomicOr(p.status, kStatusTimeout);
+    if (GATED) atomicOr(p.up_status, kStatusTimeout);
 }
 
 __device__ __forceinline__ void store_y(const GemmParams &p, int64_t idx, float v) {
@@ -230,7 +245,7 @@ __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-template <int BN, int STAGES, bool NM, bool EPI>
+template <int BN, int STAGES, bool NM, bool EPI, bool GATED>
 __global__ void __launch_bounds__(kGemmBlock<NM, EPI>, 1)
 hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ GemmParams p) {
     using C = GemmCfg<BN, STAGES>;
@@ -265,7 +280,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         if (!(chain & kChainLead)) pdl_trigger();
         // the packed weights and table are final once the ready flag is seen;
         // otherwise (the packer may be the kernel just before) wait first
-        if (ld_acquire_gpu(p.ready) == 0u) pdl_wait();
+        if (ld_acquire_gpu(p.ready) == 0u || (GATED && ld_acquire_gpu(p.up_ready) == 0u)) pdl_wait();
         else waited = chain & kChainFollow;  // X is complete when a follower starts
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -279,16 +294,19 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             mbar_init(&tab_full[b], 1);
         }
         *never_flag = 0u;
-        *abort_flag = (*reinterpret_cast<volatile uint32_t *>(p.status) & kStatusTimeout) ? 1u : 0u;
+        uint32_t raised = *reinterpret_cast<volatile uint32_t *>(p.status);
+        if (GATED) raised |= *reinterpret_cast<volatile uint32_t *>(p.up_status);
+        *abort_flag = (raised & kStatusTimeout) ? 1u : 0u;
         fence_mbar_init();
         // the first two segments' table entries start moving before anything else
         if (!*abort_flag) {
             Segment g0;
-            for (int i = 0; i < 2 && get_segment(p, cta, i, g0); ++i) {
+            for (int i = 0; i < 2 && get_segment<GATED>(p, cta, i, g0); ++i) {
                 const uint32_t nbytes = static_cast<uint32_t>(g0.ks1 - g0.ks0) * 8u;
                 mbar_arrive_expect_tx(&tab_full[i], nbytes);
                 bulk_g2s(tab_buf + i * kMaxTableSteps,
-                         p.table + static_cast<int64_t>(g0.band) * p.nsteps + g0.ks0, nbytes, &tab_full[i]);
+                         (GATED && i ? p.up_table : p.table) + static_cast<int64_t>(g0.band) * p.nsteps + g0.ks0,
+                         nbytes, &tab_full[i]);
             }
         }
     }
@@ -324,10 +342,11 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 const uint32_t nbytes = static_cast<uint32_t>(g.ks1 - g.ks0) * 8u;
                 mbar_arrive_expect_tx(&tab_full[buf], nbytes);
                 bulk_g2s(tab_buf + buf * kMaxTableSteps,
-                         p.table + static_cast<int64_t>(g.band) * p.nsteps + g.ks0, nbytes, &tab_full[buf]);
+                         (GATED && buf ? p.up_table : p.table) + static_cast<int64_t>(g.band) * p.nsteps + g.ks0,
+                         nbytes, &tab_full[buf]);
             };
-            bool have = get_segment(p, cta, 0, sg);  // tables 0 and 1 were fetched at start
-            bool have_nx = have && get_segment(p, cta, 1, nx);
+            bool have = get_segment<GATED>(p, cta, 0, sg);  // tables 0 and 1 were fetched at start
+            bool have_nx = have && get_segment<GATED>(p, cta, 1, nx);
             int tabs_issued = (have ? 1 : 0) + (have_nx ? 1 : 0);
             // X tiles of the stages armed before griddepcontrol.wait
             int pend_s[STAGES], pend_t[STAGES], pend_pr[STAGES];
@@ -347,6 +366,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                     break;
                 }
                 const uint64_t *tab = tab_buf + buf * kMaxTableSteps;
+                const uint8_t *packed = GATED && buf ? p.up_packed : p.packed;
                 for (int pr = sg.ks0 / 2; pr < sg.ks1 / 2; ++pr) {
                     const int s = it % STAGES;
                     const uint32_t ph = (it / STAGES) & 1u;
@@ -372,11 +392,11 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                         const uint32_t b0 = (c0 & kEntryNM48) ? kNM48StepBytes : kDenseStepBytes;
                         const uint32_t b1 = (c1 & kEntryNM48) ? kNM48StepBytes : kDenseStepBytes;
                         mbar_arrive_expect_tx(&full[s], b0 + b1 + C::kBBytes);
-                        bulk_g2s(st, p.packed + (c0 & kEntryOffsetMask), b0, &full[s]);
-                        bulk_g2s(st + kDenseStepBytes, p.packed + (c1 & kEntryOffsetMask), b1, &full[s]);
+                        bulk_g2s(st, packed + (c0 & kEntryOffsetMask), b0, &full[s]);
+                        bulk_g2s(st + kDenseStepBytes, packed + (c1 & kEntryOffsetMask), b1, &full[s]);
                     } else {
                         mbar_arrive_expect_tx(&full[s], bytes + C::kBBytes);
-                        bulk_g2s(st, p.packed + first, bytes, &full[s]);
+                        bulk_g2s(st, packed + first, bytes, &full[s]);
                     }
                     if (waited) {
                         tma_load_3d(st + C::kABytes, &tmap_x, 0, sg.ttile * BN, 2 * pr, &full[s]);
@@ -392,7 +412,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 have = have_nx;
                 if (have) {
                     Segment n2;
-                    have_nx = get_segment(p, cta, i + 2, n2);
+                    have_nx = get_segment<GATED>(p, cta, i + 2, n2);
                     if (have_nx) {
                         fetch_table(n2, buf);
                         ++tabs_issued;
@@ -407,7 +427,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 mbar_wait_bounded(&tab_full[j & 1], (j >> 1) & 1u, never_flag, kWaitLimitNs / 4);
             if (!ok) {
                 *abort_flag = 1u;
-                atomicOr(p.status, kStatusTimeout);
+                raise_timeout<GATED>(p);
             }
             // Drain: the last phase issued on every stage must have landed
             // before the CTA exits (a no-op when the MMA thread consumed all).
@@ -424,7 +444,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             int it = 0;
             bool ok = true;
             Segment sg;
-            for (int i = 0; ok && get_segment(p, cta, i, sg); ++i) {
+            for (int i = 0; ok && get_segment<GATED>(p, cta, i, sg); ++i) {
                 const int buf = i & 1;
                 if (i >= 2 && !mbar_wait_bounded(&acc_empty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag,
                                                  kWaitLimitNs)) {
@@ -484,7 +504,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             }
             if (!ok) {
                 *abort_flag = 1u;
-                atomicOr(p.status, kStatusTimeout);
+                raise_timeout<GATED>(p);
             }
         }
     } else if (NM && warp >= 6 && warp < 6 + kConvWarps) {
@@ -499,7 +519,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 int it = 0;
                 bool ok = true;
                 Segment sg;
-                for (int i = 0; ok && get_segment(p, cta, i, sg); ++i) {
+                for (int i = 0; ok && get_segment<GATED>(p, cta, i, sg); ++i) {
                     for (int pr = sg.ks0 / 2; pr < sg.ks1 / 2; ++pr, ++it) {
                         const int s = it % STAGES;
                         const uint32_t ph = (it / STAGES) & 1u;
@@ -528,7 +548,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 }
                 if (!ok) {
                     *abort_flag = 1u;
-                    atomicOr(p.status, kStatusTimeout);
+                    raise_timeout<GATED>(p);
                 }
             }
         }
@@ -542,8 +562,10 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         constexpr int kChunkStep = EPI ? 32 : 16;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        // gated: the gate's activated values, held from a tile's first piece to its second
+        [[maybe_unused]] uint32_t held[BN / 32][16];
         Segment sg;
-        for (int i = 0; get_segment(p, cta, i, sg); ++i) {
+        for (int i = 0; get_segment<GATED>(p, cta, i, sg); ++i) {
             const int buf = i & 1;
             // bounded by time only: the MMA thread commits acc_full even when
             // it gave up, so no MMA can be in flight at deallocation
@@ -551,7 +573,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             tc_fence_after();
             if (!ok) {
                 *abort_flag = 1u;
-                atomicOr(p.status, kStatusTimeout);
+                raise_timeout<GATED>(p);
                 break;
             }
             const bool live = *abort_flag == 0;
@@ -561,7 +583,20 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             float *part = (sg.nsegs > 1) ? p.partial + static_cast<int64_t>(sg.slot) * BN * kBand
                                          : nullptr;
             const bool whole = EPI && !part;  // this CTA's sums are the product's
-            if constexpr (EPI) {
+            if constexpr (GATED) {
+                if (live) {
+                    auto sums = [&](int c0, float(&v)[16]) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(lane_base + buf * BN + c0, r);
+                        tmem_ld_wait(r);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
+                    };
+                    const float bias = epi_bias(buf ? p.up_epi : p.epi, n);
+                    gated_piece(p.epi, p.Y, p.y_fp32, buf, lane_base + buf * BN, c_first / 16, m_base, m_valid, n, bias,
+                                held, sums);
+                }
+            } else if constexpr (EPI) {
                 if (whole && live) {
                     uint32_t add[16];
                     epi_fetch(p.epi, p.N, m_base + c_first, n, m_valid - c_first, add);
@@ -771,12 +806,14 @@ OneBand one_band_estimate(const GemmLaunch &g, int bn, bool nm, int peers = 1) {
     return tiles >= 2 * sms || whole <= peers * stream ? OneBand{whole, true} : OneBand{stream, false};
 }
 
-template <int BN, int STAGES, bool NM, bool EPI>
-cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
+// GATED: gs[0] the gate, gs[1] the up projection, whole tiles.
+template <int BN, int STAGES, bool NM, bool EPI, bool GATED = false>
+cudaError_t run_mode(const GemmLaunch *gs, int ctas_per_sm, cudaStream_t stream) {
+    const GemmLaunch &g = gs[0];
     using C = GemmCfg<BN, STAGES>;
     constexpr int kSmem = C::kSmemBytes + (NM ? kLutBytes : 0);
     static_assert(kSmem <= 232448, "shared memory per CTA");
-    const cudaError_t attr_err = allow_smem<hybrid_gemm_kernel<BN, STAGES, NM, EPI>>(kSmem);
+    const cudaError_t attr_err = allow_smem<hybrid_gemm_kernel<BN, STAGES, NM, EPI, GATED>>(kSmem);
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap map;
     if (!make_x_map(&map, g.X, g.M, g.K, BN)) return cudaErrorInvalidValue;
@@ -796,11 +833,17 @@ cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) 
     p.stall_first_kstep = g.stall_first_kstep;
     p.epi = g.epi;
     p.chain = g.chain;
+    const GemmLaunch &up = gs[GATED ? 1 : 0];
+    p.up_packed = up.packed;
+    p.up_table = up.table;
+    p.up_status = up.status;
+    p.up_ready = up.ready;
+    p.up_epi = up.epi;
     const int64_t tiles = static_cast<int64_t>(p.bands) * p.ttiles;
     const int64_t slots = static_cast<int64_t>(g.num_sms) * ctas_per_sm;
     // whole tiles when there are at least two waves of them, stream-K otherwise
     // (with an epilogue: whole tiles also where they are estimated faster)
-    const bool sk = tiles < 2 * slots && !(EPI && one_band_estimate(g, BN, NM, g.peers).whole);
+    const bool sk = !GATED && tiles < 2 * slots && !(EPI && one_band_estimate(g, BN, NM, g.peers).whole);
     p.stream_k = sk ? 1 : 0;
     p.units = tiles * (p.nsteps / 2);
     // stream-K: at most 62 CTAs per tile, so a tile's partials fit the fix-up's slot list
@@ -833,7 +876,7 @@ cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, hybrid_gemm_kernel<BN, STAGES, NM, EPI>, map, p);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, hybrid_gemm_kernel<BN, STAGES, NM, EPI, GATED>, map, p);
     if (err == cudaSuccess) note_launches(1);
     if (err == cudaSuccess && sk) {
         cfg.gridDim = dim3(static_cast<unsigned>((BN * kBand + 255) / 256), static_cast<unsigned>(tiles));
@@ -852,18 +895,18 @@ cudaError_t run_mode(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) 
 
 template <int BN, int STAGES, bool NM = false>
 cudaError_t run(const GemmLaunch &g, int ctas_per_sm, cudaStream_t stream) {
-    return g.epi_on ? run_mode<BN, STAGES, NM, true>(g, ctas_per_sm, stream)
-                    : run_mode<BN, STAGES, NM, false>(g, ctas_per_sm, stream);
+    return g.epi_on ? run_mode<BN, STAGES, NM, true>(&g, ctas_per_sm, stream)
+                    : run_mode<BN, STAGES, NM, false>(&g, ctas_per_sm, stream);
 }
 
 template <bool EPI>
 void preload_modes() {
     cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, false, EPI>);
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, false, EPI>);
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<160, 3, false, EPI>);
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, true, EPI>);
-    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, true, EPI>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, false, EPI, false>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, false, EPI, false>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<160, 3, false, EPI, false>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, true, EPI, false>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, true, EPI, false>);
     (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<64, EPI>);
     (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<128, EPI>);
     (void)cudaFuncGetAttributes(&a, streamk_reduce_kernel<160, EPI>);
@@ -874,6 +917,12 @@ void preload_modes() {
 void preload_hybrid_kernels() {
     preload_modes<false>();
     preload_modes<true>();
+    cudaFuncAttributes a;
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, false, true, true>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, false, true, true>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<160, 3, false, true, true>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<64, 4, true, true, true>);
+    (void)cudaFuncGetAttributes(&a, hybrid_gemm_kernel<128, 3, true, true, true>);
 }
 
 namespace {
@@ -922,6 +971,34 @@ Choice choose_kernel(const GemmLaunch &g) {
 }
 
 }  // namespace
+
+// The gated pair on the one-band kernel, two matrices of one kind (2:4 above 16
+// tokens, or 4:8): an item is a tile of both, so it takes whole tiles only.
+// Against two products and their fp32 scratch, by the fitted estimates (us, two
+// / one launch: 2432x256 M = 324 15.5 / 7.6, 1664x1024 M = 209 18.7 / 12.9, 128x896
+// M = 926 17.8 / 11.7; 4:8 2432x256 M = 324 16.9 / 11.6, 1664x1024 M = 209 26.2 / 27.4).
+bool takes_one_band_gated(const GemmLaunch *gs) {
+    const GemmLaunch &g = gs[0];
+    if (gs[0].pattern != gs[1].pattern || (g.force_kernel != 0 && g.force_kernel != 1)) return false;
+    const bool nm = g.pattern == 4;
+    if (!nm && g.M <= 16) return false;
+    const int bn = g.M <= 64 ? 64 : nm || g.M <= 128 ? 128 : 160;
+    const double sms = g.num_sms, pairs = static_cast<double>(g.K / (2 * kStep));
+    const double tiles = static_cast<double>((g.N / kBand) * ((g.M + bn - 1) / bn));
+    const double own = 4.7 + std::ceil(tiles / sms) * (2.0 * (nm ? 1.25 : 0.5) * pairs + bn * 2.5 / 160);
+    const double two = one_band_estimate(g, bn, nm).us + one_band_estimate(gs[1], bn, nm).us - 2.0 +
+                       2.5e-6 * static_cast<double>(g.M) * static_cast<double>(g.N);
+    return g.force_kernel == 1 || own <= two;
+}
+
+cudaError_t launch_one_band_gated(const GemmLaunch *gs, cudaStream_t stream) {
+    if (gs[0].pattern == 4)
+        return gs[0].M <= 64 ? run_mode<64, 4, true, true, true>(gs, 1, stream)
+                             : run_mode<128, 3, true, true, true>(gs, 1, stream);
+    if (gs[0].M <= 64) return run_mode<64, 4, false, true, true>(gs, 1, stream);
+    return gs[0].M <= 128 ? run_mode<128, 3, false, true, true>(gs, 1, stream)
+                          : run_mode<160, 3, false, true, true>(gs, 1, stream);
+}
 
 bool hybrid_chains(const GemmLaunch &g) {  // as launch_hybrid_gemm picks the kernel
     if (!g.epi_on) return false;

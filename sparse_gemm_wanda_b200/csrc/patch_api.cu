@@ -1252,12 +1252,18 @@ static patch_status gated_products(const patch_packed *const *hs, const void *X,
     const bool same_sms = hs[0]->num_sms == hs[1]->num_sms;
     const bool f8 = hs[0]->pattern == 8 && hs[1]->pattern == 8, bf = hs[0]->pattern == 2 && hs[1]->pattern == 2;
     const patchk::Epilogue es[2] = {gate, up};
+    if (!f8 && same_sms && hs[0]->pattern == 4 && hs[1]->pattern == 4) {
+        const patchk::GemmLaunch gs[2] = {gemm_launch(hs[0], X, M, Y, y_is_fp32, &es[0]),
+                                          gemm_launch(hs[1], X, M, Y, y_is_fp32, &es[1])};
+        if (patchk::takes_one_band_gated(gs)) return from_cuda(patchk::launch_one_band_gated(gs, stream));
+    }
     if (bf && same_sms) {
         const patchk::GemmLaunch gs[2] = {gemm_launch(hs[0], X, M, Y, y_is_fp32, &es[0]),
                                           gemm_launch(hs[1], X, M, Y, y_is_fp32, &es[1])};
         if (patchk::takes_split_k(M, K, force)) return from_cuda(patchk::launch_decode_group(gs, 2, stream, true));
         patchk::DuoPlan dp;
         if (patchk::plan_hybrid_gated(gs, &dp)) return from_cuda(patchk::launch_duo_group(gs, 2, dp, stream, true));
+        if (patchk::takes_one_band_gated(gs)) return from_cuda(patchk::launch_one_band_gated(gs, stream));
     }
     XCodes x;
     cudaError_t e = cudaSuccess;

@@ -166,6 +166,10 @@ struct GemmLaunch {
 enum { kChainLead = 1, kChainFollow = 2 };
 // whether launch_hybrid_gemm / launch_fp8_gemm run this product on such a kernel
 bool hybrid_chains(const GemmLaunch &g);
+// The gated pair in one launch of the one-band kernel, and whether that is
+// estimated to finish before two products.
+bool takes_one_band_gated(const GemmLaunch *gs);
+cudaError_t launch_one_band_gated(const GemmLaunch *gs, cudaStream_t stream);
 struct Fp8Launch;
 bool fp8_chains(const Fp8Launch &g);
 
