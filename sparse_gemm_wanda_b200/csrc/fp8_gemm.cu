@@ -33,6 +33,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "epilogue.cuh"
@@ -69,6 +70,12 @@ struct F8Params {
     int y_fp32;
     uint32_t *status;
     Epilogue epi;
+    // gated pairs: the up projection's (p.packed, .. are the gate's)
+    const uint8_t *up_packed;
+    const uint64_t *up_table;
+    const float *up_sw;
+    uint32_t *up_status;
+    Epilogue up_epi;
     int chain;  // kChainLead / kChainFollow, with an epilogue only
 };
 
@@ -100,7 +107,15 @@ struct F8Cfg {
     static_assert(kCols <= 512, "tensor memory holds 512 columns");
 };
 
-template <int BN, bool EPI>
+template <bool GATED>
+__device__ __forceinline__ void raise_timeout(const F8Params &p) {
+    atomicOr(p.status, kStatusTimeout);
+    if (GATED) atomicOr(p.up_status, kStatusTimeout);
+}
+
+// GATED: whole tiles, piece 2q of a CTA a tile of the gate and 2q + 1 the same
+// tile of the up projection.
+template <int BN, bool EPI, bool GATED>
 __global__ void __launch_bounds__(kF8Block<EPI>, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ F8Params p) {
     using C = F8Cfg<BN>;
@@ -132,7 +147,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             mbar_init(&acc_empty[b], EPI ? 8 : 4);  // epilogue warps
         }
         *never_flag = 0u;
-        *abort_flag = (*reinterpret_cast<volatile uint32_t *>(p.status) & kStatusTimeout) ? 1u : 0u;
+        uint32_t raised = *reinterpret_cast<volatile uint32_t *>(p.status);
+        if (GATED) raised |= *reinterpret_cast<volatile uint32_t *>(p.up_status);
+        *abort_flag = (raised & kStatusTimeout) ? 1u : 0u;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -159,12 +176,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const int w = cta + i * P;
+                const int w = cta + (GATED ? i >> 1 : i) * P;
                 if (w >= p.items) break;
                 int tile, c0, c1;
                 f8_item(p, w, tile, c0, c1);
                 const int band = tile / p.ttiles;
-                const uint64_t *tab = p.table + static_cast<int64_t>(band) * p.steps;
+                const bool up = GATED && (i & 1);
+                const uint64_t *tab = (up ? p.up_table : p.table) + static_cast<int64_t>(band) * p.steps;
+                const uint8_t *packed = up ? p.up_packed : p.packed;
                 for (int c = c0; c < c1; ++c) {
                     const int s = it % S;
                     const uint32_t ph = (it / S) & 1u;
@@ -180,12 +199,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     ++it;
                     uint8_t *st = smem + s * C::kStageBytes;
                     mbar_arrive_expect_tx(&full[s], bytes);
-                    bulk_g2s(st, p.packed + first, bytes, &full[s]);
+                    bulk_g2s(st, packed + first, bytes, &full[s]);
                 }
             }
             if (!ok) {
                 *abort_flag = 1u;
-                atomicOr(p.status, kStatusTimeout);
+                raise_timeout<GATED>(p);
             }
             // the last phase issued on every stage lands before the CTA exits
             for (int q = (it > S ? it - S : 0); q < it; ++q)
@@ -198,7 +217,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const int w = cta + i * P;
+                const int w = cta + (GATED ? i >> 1 : i) * P;
                 if (w >= p.items) break;
                 int tile, c0, c1;
                 f8_item(p, w, tile, c0, c1);
@@ -217,7 +236,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             }
             if (!ok) {
                 *abort_flag = 1u;
-                atomicOr(p.status, kStatusTimeout);
+                raise_timeout<GATED>(p);
             }
         }
     } else if (warp == 1) {
@@ -229,7 +248,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
-                const int w = cta + i * P;
+                const int w = cta + (GATED ? i >> 1 : i) * P;
                 if (w >= p.items) break;
                 int tile, c0, c1;
                 f8_item(p, w, tile, c0, c1);
@@ -275,7 +294,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             }
             if (!ok) {
                 *abort_flag = 1u;
-                atomicOr(p.status, kStatusTimeout);
+                raise_timeout<GATED>(p);
             }
         }
     } else if (!skip) {
@@ -288,8 +307,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         constexpr int kChunkStep = EPI ? 32 : 16;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        // gated: the gate's activated values, held from a tile's first piece to its second
+        [[maybe_unused]] uint32_t held[(BN + 31) / 32][16];
         for (int i = 0;; ++i) {
-            const int w = cta + i * P;
+            const int w = cta + (GATED ? i >> 1 : i) * P;
             if (w >= p.items) break;
             const int tile = w / p.ksplit;
             const int buf = i & 1;
@@ -297,14 +318,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             tc_fence_after();
             if (!ok) {
                 *abort_flag = 1u;
-                atomicOr(p.status, kStatusTimeout);
+                raise_timeout<GATED>(p);
                 break;
             }
             const int band = tile / p.ttiles, tt = tile % p.ttiles;
             const int64_t n = static_cast<int64_t>(band) * kBand + row;
             const int64_t m_base = static_cast<int64_t>(tt) * BN;
             const int m_valid = static_cast<int>(min(static_cast<int64_t>(BN), p.M - m_base));
-            const float swn = __ldg(p.sw + n);
+            const float swn = __ldg((GATED && buf ? p.up_sw : p.sw) + n);
             if (*abort_flag == 0 && p.ksplit > 1) {
                 // this range's accumulator, unscaled, into the item's slot
                 float *part = p.partial + static_cast<int64_t>(w) * BN * kBand + row;
@@ -319,8 +340,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 }
             } else if (*abort_flag != 0) {
             } else if constexpr (EPI) {
-                uint32_t add[16];
-                epi_fetch(p.epi, p.N, m_base + c_first, n, m_valid - c_first, add);
+                [[maybe_unused]] uint32_t add[16];
+                if constexpr (!GATED) epi_fetch(p.epi, p.N, m_base + c_first, n, m_valid - c_first, add);
                 auto scaled = [&](int c0, float(&v)[16]) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
@@ -332,8 +353,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     for (int q = 0; q < 16; ++q)
                         v[q] = __uint_as_float(r[q]) * swn * __shfl_sync(0xFFFFFFFFu, sxl, q);
                 };
-                epi_drain(p.epi, p.Y, p.y_fp32, p.N, c_first, kChunkStep, m_base, m_valid, n, epi_bias(p.epi, n), add,
-                          scaled);
+                if constexpr (GATED)
+                    gated_piece(p.epi, p.Y, p.y_fp32, buf, lane_base + static_cast<uint32_t>(buf * BN), c_first / 16,
+                                m_base, m_valid, n, epi_bias(buf ? p.up_epi : p.epi, n), held, scaled);
+                else
+                    epi_drain(p.epi, p.Y, p.y_fp32, p.N, c_first, kChunkStep, m_base, m_valid, n, epi_bias(p.epi, n),
+                              add, scaled);
             } else {
 #pragma unroll 1
                 for (int c0 = c_first; c0 < m_valid; c0 += kChunkStep) {
@@ -452,10 +477,11 @@ void split_tiles(const Fp8Launch &g, int tiles, int steps, int peers, int *kspli
     }
 }
 
-template <int BN, bool EPI>
-cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
+template <int BN, bool EPI, bool GATED = false>
+cudaError_t run_fp8_mode(const Fp8Launch *gs, cudaStream_t stream) {
+    const Fp8Launch &g = gs[0];
     using C = F8Cfg<BN>;
-    const cudaError_t attr_err = allow_smem<fp8_gemm_kernel<BN, EPI>>(C::kSmem);
+    const cudaError_t attr_err = allow_smem<fp8_gemm_kernel<BN, EPI, GATED>>(C::kSmem);
     if (attr_err != cudaSuccess) return attr_err;
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorInvalidValue;
@@ -487,7 +513,15 @@ cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     p.status = g.status;
     p.epi = g.epi;
     p.chain = g.chain;
-    split_tiles(g, p.tiles, p.steps, g.peers, &p.ksplit, &p.kper);
+    const Fp8Launch &up = gs[GATED ? 1 : 0];
+    p.up_packed = up.packed;
+    p.up_table = up.table;
+    p.up_sw = up.sw;
+    p.up_status = up.status;
+    p.up_epi = up.epi;
+    p.ksplit = 1;
+    p.kper = p.steps;
+    if (!GATED) split_tiles(g, p.tiles, p.steps, g.peers, &p.ksplit, &p.kper);
     p.items = p.tiles * p.ksplit;
     p.partial = nullptr;
     float *ws = nullptr;
@@ -509,7 +543,7 @@ cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
     kcfg.stream = stream;
     kcfg.attrs = attr;
     kcfg.numAttrs = 1;
-    cudaError_t err = cudaLaunchKernelEx(&kcfg, fp8_gemm_kernel<BN, EPI>, map, p);
+    cudaError_t err = cudaLaunchKernelEx(&kcfg, fp8_gemm_kernel<BN, EPI, GATED>, map, p);
     if (err == cudaSuccess) note_launches(1);
     if (err == cudaSuccess && p.ksplit > 1) {
         cudaLaunchConfig_t cfg = {};
@@ -531,13 +565,14 @@ cudaError_t run_fp8_mode(const Fp8Launch &g, cudaStream_t stream) {
 
 template <int BN>
 cudaError_t run_fp8(const Fp8Launch &g, cudaStream_t stream) {
-    return g.epi_on ? run_fp8_mode<BN, true>(g, stream) : run_fp8_mode<BN, false>(g, stream);
+    return g.epi_on ? run_fp8_mode<BN, true>(&g, stream) : run_fp8_mode<BN, false>(&g, stream);
 }
 
 template <int BN, bool EPI>
 void preload_fp8() {
     cudaFuncAttributes a;
-    (void)cudaFuncGetAttributes(&a, fp8_gemm_kernel<BN, EPI>);
+    (void)cudaFuncGetAttributes(&a, fp8_gemm_kernel<BN, EPI, false>);
+    if (EPI) (void)cudaFuncGetAttributes(&a, fp8_gemm_kernel<BN, true, true>);
     (void)cudaFuncGetAttributes(&a, fp8_splitk_reduce_kernel<BN, EPI>);
 }
 
@@ -609,6 +644,30 @@ bool takes_duo_fp8_gated(const Fp8Launch *gs) {
     if (g.M <= 64) return false;
     const DuoFp8Plan dp = plan_duo_fp8(g.N, g.M, g.num_sms, gs[0].all_sparse && gs[1].all_sparse);
     return dp.bn > 0 && duo_fp8_us(g, dp, 2) <= fp8_us(gs[0]) + fp8_us(gs[1]);
+}
+
+// The gated pair on the one-band kernel: whole tiles of both matrices, against two
+// products and their fp32 scratch by the fitted estimates (us, two / one launch:
+// X quantised: 2432x256 M = 324 22.3 / 14.9, 1664x1024 M = 209 20.9 / 17.1).
+bool takes_one_band_gated_fp8(const Fp8Launch *gs) {
+    const Fp8Launch &g = gs[0];
+    if (g.force_kernel != 0 && g.force_kernel != 1) return false;
+    const int bn = g.M <= 64 ? 64 : g.M <= 128 ? 128 : 240;
+    const double cols = static_cast<double>(std::min<int64_t>(g.M, bn));
+    const double tiles = static_cast<double>((g.N / kBand) * ((g.M + bn - 1) / bn));
+    const double waves = std::ceil(tiles / g.num_sms), steps = static_cast<double>(g.K / kF8Step);
+    const double own = 3.0 + waves * (0.045 * cols + 2 * 0.31 * steps);
+    const double two = fp8_us(gs[0]) + fp8_us(gs[1]) - 2.0 +
+                       2.5e-6 * static_cast<double>(g.M) * static_cast<double>(g.N);
+    return g.force_kernel == 1 || own <= two;
+}
+
+cudaError_t launch_one_band_gated_fp8(const Fp8Launch *gs, cudaStream_t stream) {
+    const Fp8Launch &g = gs[0];
+    if (g.K % kF8Step != 0 || g.N % kBand != 0 || g.M < 1) return cudaErrorInvalidValue;
+    if (g.M <= 64) return run_fp8_mode<64, true, true>(gs, stream);
+    if (g.M <= 128) return run_fp8_mode<128, true, true>(gs, stream);
+    return run_fp8_mode<240, true, true>(gs, stream);
 }
 
 bool fp8_chains(const Fp8Launch &g) { return g.epi_on && !takes_duo_fp8(g); }

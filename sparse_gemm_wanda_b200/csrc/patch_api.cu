@@ -1283,6 +1283,8 @@ static patch_status gated_products(const patch_packed *const *hs, const void *X,
             dp = patchk::plan_duo_fp8(N, M, gs[0].num_sms, gs[0].all_sparse && gs[1].all_sparse);
             if (dp.bn > 0) return free_codes(x, patchk::launch_duo_fp8_group(gs, 2, dp, stream, true), stream);
         }
+        if (same_sms && patchk::takes_one_band_gated_fp8(gs))
+            return free_codes(x, patchk::launch_one_band_gated_fp8(gs, stream), stream);
         X = x.q;
         x_scales = x.s;
     }

@@ -320,6 +320,10 @@ bool takes_duo_fp8(const Fp8Launch &g);
 // whether one two-SM launch is estimated to finish a gated pair no later than
 // two products one after another
 bool takes_duo_fp8_gated(const Fp8Launch *gs);
+// the pair in one launch of the one-band kernel, and whether that is estimated
+// to finish before two products
+bool takes_one_band_gated_fp8(const Fp8Launch *gs);
+cudaError_t launch_one_band_gated_fp8(const Fp8Launch *gs, cudaStream_t stream);
 
 // Two-SM FP8 prefill GEMM (csrc/prefill_duo_fp8.cu): bands 2p, 2p+1 of the
 // prefill table on a CTA pair, two 128-column k-steps per stage.
