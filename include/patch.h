@@ -551,7 +551,7 @@ patch_status patch_hybrid_gated(const patch_packed *Wgate, const patch_packed *W
                                 int32_t bias_is_fp32, int32_t activation, void *stream);
 
 typedef enum {
-    PATCH_NORM_NONE = 0,
+    PATCH_NORM_NONE = 0, /* v; the spec's other fields are not used              */
     PATCH_NORM_RMS = 1,  /* v / sqrt(mean(v^2) + eps) * weight + bias            */
     PATCH_NORM_LAYER = 2 /* (v - mean) / sqrt(var + eps) * weight + bias         */
 } patch_norm_kind;

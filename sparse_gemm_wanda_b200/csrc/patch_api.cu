@@ -1359,9 +1359,16 @@ patch_status patch_hybrid_gated(const patch_packed *Wgate, const patch_packed *W
 
 // ------------------------------------------------------- norms of a block
 static bool norm_ok(const patch_norm &n) {
-    return n.kind >= PATCH_NORM_NONE && n.kind <= PATCH_NORM_LAYER && flag_ok(n.is_fp32) &&
-           (n.kind == PATCH_NORM_NONE || n.eps >= 0.0f) && aligned_to(n.weight, real_bytes(n.is_fp32)) &&
-           aligned_to(n.bias, real_bytes(n.is_fp32));
+    if (n.kind == PATCH_NORM_NONE) return true;
+    return n.kind > PATCH_NORM_NONE && n.kind <= PATCH_NORM_LAYER && flag_ok(n.is_fp32) && n.eps >= 0.0f &&
+           aligned_to(n.weight, real_bytes(n.is_fp32)) && aligned_to(n.bias, real_bytes(n.is_fp32));
+}
+
+// The kernels choose by type and multiply by a weight wherever there is one:
+// a norm that is off has none, whatever its fields hold.
+static patchk::NormSpec norm_spec(const patch_norm &n) {
+    if (n.kind == PATCH_NORM_NONE) return patchk::NormSpec{nullptr, nullptr, 0.0f, patchk::kNormNone, 0};
+    return patchk::NormSpec{n.weight, n.bias, n.eps, n.kind, n.is_fp32};
 }
 
 patch_status patch_block_norm(const patch_block_norm_args *a, int64_t M, int64_t C, void *stream_v) {
@@ -1412,8 +1419,8 @@ patch_status patch_block_norm(const patch_block_norm_args *a, int64_t M, int64_t
     p.z_scales = a->z_scales;
     p.gate_tokens = a->gate ? a->gate_tokens : 1;
     p.M = M;
-    p.post = patchk::NormSpec{a->post.weight, a->post.bias, a->post.eps, a->post.kind, a->post.is_fp32};
-    p.pre = patchk::NormSpec{a->pre.weight, a->pre.bias, a->pre.eps, a->pre.kind, a->pre.is_fp32};
+    p.post = norm_spec(a->post);
+    p.pre = norm_spec(a->pre);
     p.scale = a->scale;
     p.C = static_cast<int>(C);
     p.branch_fp32 = a->branch_is_fp32;
