@@ -76,7 +76,8 @@ struct F8Params {
     const float *up_sw;
     uint32_t *up_status;
     Epilogue up_epi;
-    int chain;  // kChainLead / kChainFollow, with an epilogue only
+    int chain;  // kChainLead, or kChainFollow and kChainLast, with an epilogue only
+    uint32_t *chain_flag;
 };
 
 // Work item w: tile w / ksplit, k-steps [c0, c1) of it.
@@ -130,6 +131,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     volatile uint32_t *abort_flag = tmem_slot + 1;
     volatile uint32_t *never_flag = tmem_slot + 2;
+    volatile uint32_t *early_flag = tmem_slot + 3;  // a follower that may run ahead of its wait
     uint64_t *stage_info = reinterpret_cast<uint64_t *>(tmem_slot + 4);  // [S]
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -147,6 +149,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             mbar_init(&acc_empty[b], EPI ? 8 : 4);  // epilogue warps
         }
         *never_flag = 0u;
+        // X, the weights, the residual and the bias are then complete and visible
+        *early_flag = (chain & kChainFollow) && ld_acquire_gpu(p.chain_flag) != 0u ? 1u : 0u;
         uint32_t raised = *reinterpret_cast<volatile uint32_t *>(p.status);
         if (GATED) raised |= *reinterpret_cast<volatile uint32_t *>(p.up_status);
         *abort_flag = (raised & kStatusTimeout) ? 1u : 0u;
@@ -162,17 +166,22 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const bool skip = *abort_flag != 0;
+    const bool early = EPI && *early_flag != 0;
     if (threadIdx.x == 64 && ((chain & kChainLead) || (chain && skip))) {  // an epilogue thread
         pdl_wait();
-        if (chain & kChainLead) pdl_trigger();
+        if (chain & kChainLead) {
+            if (cta == 0) raise_chain_flag(p.chain_flag);
+            pdl_trigger();
+        }
     }
 
     if (warp == 0) {
         if (lane == 0 && !skip) {
             // ------------------------------------------------------ producer
             // launched as a programmatic dependent: global memory after the wait
-            // (a follower starts after the wait of the product before it)
-            if (!(chain & kChainFollow)) pdl_wait();
+            // (early: behind the wait of the chain's first product)
+            if (early) fence_async_global();
+            else pdl_wait();
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
@@ -213,7 +222,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     } else if (warp == 6) {
         if (lane == 0 && !skip) {
             // ---------------------------------------------------- X producer
-            if (!(chain & kChainFollow)) pdl_wait();  // the codes are written by the kernel just before
+            // the codes are written by the kernel just before
+            if (early) fence_async_global();
+            else pdl_wait();
             int it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
@@ -300,7 +311,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     } else if (!skip) {
         // ------------------------------------------------------- epilogue
         // Y and the partial slots may still be used by earlier kernels
-        const bool late = (chain & kChainFollow) && p.ksplit == 1 && !p.epi.mul;
+        const bool late = early && p.ksplit == 1 && !p.epi.mul;
         if (!late) pdl_wait();
         const int quad = warp % 4;
         const int c_first = EPI && warp >= 7 ? 16 : 0;  // the second group's first chunk
@@ -325,7 +336,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             const int64_t n = static_cast<int64_t>(band) * kBand + row;
             const int64_t m_base = static_cast<int64_t>(tt) * BN;
             const int m_valid = static_cast<int>(min(static_cast<int64_t>(BN), p.M - m_base));
-            const float swn = __ldg((GATED && buf ? p.up_sw : p.sw) + n);
+            // (scales by plain loads: the read-only path takes no part in a follower's acquire)
+            const float swn = (GATED && buf ? p.up_sw : p.sw)[n];
             if (*abort_flag == 0 && p.ksplit > 1) {
                 // this range's accumulator, unscaled, into the item's slot
                 float *part = p.partial + static_cast<int64_t>(w) * BN * kBand + row;
@@ -347,7 +359,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
                     // token scales of the chunk: lane l holds column l % 16's
                     const int ml = c0 + (lane & 15);
-                    const float sxl = ml < m_valid ? __ldg(p.sx + m_base + ml) : 0.0f;
+                    const float sxl = ml < m_valid ? p.sx[m_base + ml] : 0.0f;
                     tmem_ld_wait(r);
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
@@ -379,6 +391,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         }
         if (late) pdl_wait();  // done only when the product before is
     }
+    if (threadIdx.x == 64 && (chain & kChainLast) && cta == 0) *p.chain_flag = 0u;  // past its wait
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -513,6 +526,7 @@ cudaError_t run_fp8_mode(const Fp8Launch *gs, cudaStream_t stream) {
     p.status = g.status;
     p.epi = g.epi;
     p.chain = g.chain;
+    p.chain_flag = g.chain_flag;
     const Fp8Launch &up = gs[GATED ? 1 : 0];
     p.up_packed = up.packed;
     p.up_table = up.table;
@@ -674,7 +688,7 @@ bool fp8_chains(const Fp8Launch &g) { return g.epi_on && !takes_duo_fp8(g); }
 
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream) {
     if (g.K % kF8Step != 0 || g.N % kBand != 0 || g.M < 1) return cudaErrorInvalidValue;
-    if (g.chain && !fp8_chains(g)) return cudaErrorInvalidValue;
+    if (g.chain && (!g.chain_flag || !fp8_chains(g))) return cudaErrorInvalidValue;
     if (takes_duo_fp8(g)) {
         const DuoFp8Plan dp = plan_duo_fp8(g.N, g.M, g.num_sms, g.all_sparse != 0);
         if (dp.bn > 0) return launch_duo_fp8(g, dp, stream);

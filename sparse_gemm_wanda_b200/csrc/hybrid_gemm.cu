@@ -129,7 +129,8 @@ struct GemmParams {
     uint32_t *up_status;
     const uint32_t *up_ready;
     Epilogue up_epi;
-    int chain;  // kChainLead / kChainFollow, with an epilogue only
+    int chain;  // kChainLead, or kChainFollow and kChainLast, with an epilogue only
+    uint32_t *chain_flag;
 };
 
 // One piece of work of a CTA: k-steps [ks0, ks1) of tile (band, ttile).
@@ -266,6 +267,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cread + STAGES);
     volatile uint32_t *abort_flag = tmem_slot + 1;  // raised by any role that gives up
     volatile uint32_t *never_flag = tmem_slot + 2;  // stays 0: time-only bounded waits
+    volatile uint32_t *early_flag = tmem_slot + 3;  // a follower that may run ahead of its wait
     // per stage, written by the producer before it arms the stage: the pair's two
     // table entries and the stream offset of its first byte
     uint64_t *stage_info = reinterpret_cast<uint64_t *>(tmem_slot + 4);
@@ -278,10 +280,14 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     const int chain = EPI ? p.chain : 0;
     if (threadIdx.x == 0) {
         if (!(chain & kChainLead)) pdl_trigger();
-        // the packed weights and table are final once the ready flag is seen;
-        // otherwise (the packer may be the kernel just before) wait first
-        if (ld_acquire_gpu(p.ready) == 0u || (GATED && ld_acquire_gpu(p.up_ready) == 0u)) pdl_wait();
-        else waited = chain & kChainFollow;  // X is complete when a follower starts
+        // a follower that sees its chain's flag: the weights, X, the residual and
+        // the bias are complete and visible
+        *early_flag = (chain & kChainFollow) && ld_acquire_gpu(p.chain_flag) != 0u ? 1u : 0u;
+        // otherwise the packed weights and table are final once the ready flag is
+        // seen; else (the packer may be the kernel just before) wait first
+        if (*early_flag) fence_async_global();
+        else if (ld_acquire_gpu(p.ready) == 0u || (GATED && ld_acquire_gpu(p.up_ready) == 0u)) pdl_wait();
+        else waited = false;
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -324,9 +330,13 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const bool skip = *abort_flag != 0;
+    const bool early = EPI && *early_flag != 0;
     if (threadIdx.x == 64 && ((chain & kChainLead) || (chain && skip))) {  // an epilogue thread
         pdl_wait();
-        if (chain & kChainLead) pdl_trigger();
+        if (chain & kChainLead) {
+            if (cta == 0) raise_chain_flag(p.chain_flag);
+            pdl_trigger();
+        }
     }
 
     if (warp == 0) {
@@ -555,7 +565,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     } else if (!skip) {
         // ------------------------------------------------------- epilogue
         // Y and the partials may still be in use by earlier kernels
-        const bool late = (chain & kChainFollow) && !p.stream_k && !p.epi.mul;
+        const bool late = early && !p.stream_k && !p.epi.mul;
         if (!late) pdl_wait();
         const int quad = warp % 4;  // TMEM lanes 32*quad .. 32*quad+31
         const int c_first = EPI && warp >= 6 ? 16 : 0;  // the second group's first chunk
@@ -635,6 +645,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         }
         if (late) pdl_wait();  // done only when the product before is
     }
+    if (threadIdx.x == 64 && (chain & kChainLast) && cta == 0) *p.chain_flag = 0u;  // past its wait
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -833,6 +844,7 @@ cudaError_t run_mode(const GemmLaunch *gs, int ctas_per_sm, cudaStream_t stream)
     p.stall_first_kstep = g.stall_first_kstep;
     p.epi = g.epi;
     p.chain = g.chain;
+    p.chain_flag = g.chain_flag;
     const GemmLaunch &up = gs[GATED ? 1 : 0];
     p.up_packed = up.packed;
     p.up_table = up.table;
@@ -1009,7 +1021,7 @@ bool hybrid_chains(const GemmLaunch &g) {  // as launch_hybrid_gemm picks the ke
 }
 
 cudaError_t launch_hybrid_gemm(const GemmLaunch &g, cudaStream_t stream) {
-    if (g.chain && !hybrid_chains(g)) return cudaErrorInvalidValue;
+    if (g.chain && (!g.chain_flag || !hybrid_chains(g))) return cudaErrorInvalidValue;
     if (g.pattern == 4) {
         // 4:8 handles: the one-band kernel with converter warps, every M
         // (stream-K over (tile, k-pair) units when tiles are few)

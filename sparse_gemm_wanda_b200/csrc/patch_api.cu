@@ -40,7 +40,7 @@ struct patch_packed {
     int dec_cp, dec_cpb, dec_nchunks;
     int duo_ok;                // even band count: the prefill table pairs bands 2p, 2p+1
     int max_pair_bytes;        // largest k-pair the prefill table points to
-    uint32_t *status;          // device: status word, pack counter, ready flag
+    uint32_t *status;          // device: status word, pack counter, ready flag, chunk counter, chain flag
     int num_sms;
     cudaMemPool_t pool;
     int64_t bands;
@@ -177,6 +177,31 @@ template <class Launch>
 void set_epilogue(Launch &g, const patchk::Epilogue *epi) {
     g.epi_on = epi ? 1 : 0;
     if (epi) g.epi = *epi;
+}
+
+// A product's place among products that run side by side (see kChainLead).
+struct Chain {
+    int place = 0;
+    int peers = 1;
+    uint32_t *flag = nullptr;
+};
+
+// place i of `count` products led by `lead`'s
+Chain chain_of(const patch_packed *lead, int i, int count) {
+    const int last = i + 1 == count ? patchk::kChainLast : 0;
+    return {i ? patchk::kChainFollow | last : patchk::kChainLead, count, lead->status + 4};
+}
+
+template <class Launch>
+void put_chain(Launch &g, const Chain &c) {
+    g.chain = c.place;
+    g.peers = c.peers;
+    g.chain_flag = c.flag;
+}
+
+// A chain that ended early, its first kernel enqueued: the flag is lowered behind it.
+void end_chain(const Chain &c, cudaStream_t stream) {
+    if (c.flag) (void)cudaMemsetAsync(c.flag, 0, sizeof(uint32_t), stream);
 }
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -642,7 +667,7 @@ static patch_status pack_group_impl(const void *const *Ws, const uint32_t *const
         h->ptable = reinterpret_cast<uint64_t *>(h->base + off_ptable);
         patchk::PackPlan *pd = reinterpret_cast<patchk::PackPlan *>(h->base + off_plan);
         h->workspace = reinterpret_cast<float *>(h->base + off_ws);
-        // status word | (unused) | ready flag | decode chunk counter
+        // status word | (unused) | ready flag | decode chunk counter | chain flag
         // (zeroed by the plan launch, before any kernel reads them)
         h->status = reinterpret_cast<uint32_t *>(h->base + off_status);
         pa[i] = patchk::PlanArgs{maps[i], N, K, static_cast<int>(shp.tile_n), static_cast<int>(shp.tile_k),
@@ -991,7 +1016,7 @@ static patch_status free_codes(const XCodes &x, cudaError_t e, cudaStream_t stre
 }
 
 static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
-                             int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, int chain, int peers) {
+                             int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, const Chain &chain) {
     XCodes x;
     cudaError_t e = codes_of(Wp, X, x_scales, M, &x, stream);
     const int force = g_test_kernel.load(std::memory_order_relaxed);
@@ -1002,8 +1027,7 @@ static patch_status fp8_gemm(const patch_packed *Wp, const void *X, const float 
         e = patchk::launch_decode_f8(&g, 1, stream);
     } else if (e == cudaSuccess) {
         patchk::Fp8Launch g = fp8_launch(Wp, x.q, x.s, M, Y, y_is_fp32, epi);
-        g.chain = chain;
-        g.peers = peers;
+        put_chain(g, chain);
         e = patchk::launch_fp8_gemm(g, stream);
     }
     return free_codes(x, e, stream);
@@ -1048,12 +1072,11 @@ static patchk::GemmLaunch gemm_launch(const patch_packed *Wp, const void *X_bf16
 }
 
 static patch_status product_one(const patch_packed *Wp, const void *X, const float *x_scales, int64_t M, void *Y,
-                                int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream, int chain = 0,
-                                int peers = 1) {
-    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, epi, stream, chain, peers);
+                                int32_t y_is_fp32, const patchk::Epilogue *epi, cudaStream_t stream,
+                                const Chain &chain = Chain()) {
+    if (Wp->pattern == 8) return fp8_gemm(Wp, X, x_scales, M, Y, y_is_fp32, epi, stream, chain);
     patchk::GemmLaunch g = gemm_launch(Wp, X, M, Y, y_is_fp32, epi);
-    g.chain = chain;
-    g.peers = peers;
+    put_chain(g, chain);
     return from_cuda(patchk::launch_hybrid_gemm(g, stream));
 }
 
@@ -1170,8 +1193,9 @@ static patch_status products(const patch_packed *const *Wps, int32_t count, cons
         bool side = epis && count > 1;
         for (int i = 0; i < count && side; ++i) side = chains(Wps[i], X, x_scales, M, epi(i));
         for (int i = 0; i < count && st == PATCH_OK; ++i) {
-            const int chain = !side ? 0 : i ? patchk::kChainFollow : patchk::kChainLead;
-            st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream, chain, side ? count : 1);
+            const Chain chain = side ? chain_of(Wps[0], i, count) : Chain();
+            st = product_one(Wps[i], X, x_scales, M, Ys[i], y_is_fp32, epi(i), stream, chain);
+            if (st != PATCH_OK) end_chain(chain, stream);
         }
         const patch_status st2 = free_codes(x, cudaSuccess, stream);
         return st != PATCH_OK ? st : st2;
@@ -1296,9 +1320,14 @@ static patch_status gated_products(const patch_packed *const *hs, const void *X,
     first.ldy = N;
     second.mul = held;
     const bool both = chains(hs[0], X, x_scales, M, &first) && chains(hs[1], X, x_scales, M, &second);
-    patch_status st = product_one(hs[0], X, x_scales, M, held, 1, &first, stream, both ? patchk::kChainLead : 0);
-    if (st == PATCH_OK)
-        st = product_one(hs[1], X, x_scales, M, Y, y_is_fp32, &second, stream, both ? patchk::kChainFollow : 0);
+    patch_status st = PATCH_OK;
+    for (int i = 0; i < 2 && st == PATCH_OK; ++i) {
+        Chain chain = both ? chain_of(hs[0], i, 2) : Chain();
+        chain.peers = 1;  // the second waits for the first's values: each picks its kernel as if alone
+        st = i ? product_one(hs[1], X, x_scales, M, Y, y_is_fp32, &second, stream, chain)
+               : product_one(hs[0], X, x_scales, M, held, 1, &first, stream, chain);
+        if (st != PATCH_OK) end_chain(chain, stream);
+    }
     const patch_status st2 = free_codes(x, cudaFreeAsync(held, stream), stream);
     return st != PATCH_OK ? st : st2;
 }

@@ -61,6 +61,14 @@ __device__ __forceinline__ void st_release_gpu(uint32_t *p, uint32_t v) {
     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// Hands the writes made visible to this thread by its wait to the followers of
+// a chain (see kChainLead).
+__device__ __forceinline__ void raise_chain_flag(uint32_t *flag) { st_release_gpu(flag, 1u); }
+
+// Orders this thread's later async-proxy reads of global memory (bulk and
+// tensor copies) behind the generic-proxy writes it has acquired.
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
                  : "memory");

@@ -152,18 +152,26 @@ struct GemmLaunch {
     const float *f8_sx;      // [M] token scales
     int epi_on = 0;          // Y takes the epilogue `epi` (else the plain sums, rows of N)
     Epilogue epi;
-    int chain = 0;           // kChainLead / kChainFollow (only where hybrid_chains)
+    int chain = 0;           // kChainLead, or kChainFollow and kChainLast (only where hybrid_chains)
+    uint32_t *chain_flag = nullptr;  // of the chain's first handle
     int peers = 1;           // products that run side by side, this one included
 };
 
 // Products that read the same X, launched one after another on the one-band
 // kernels, run side by side where the earlier ones leave SMs idle: the first
 // (lead) lets its dependent launch only once its own wait for the stream's
-// earlier work has returned, so X, Y and the residual are ready when a follower
-// starts.  A follower reads X at once; its epilogue waits for the kernel before
-// it where it may share memory with that (split ranges' partials, the gate's
-// values), else only at its end, so the chain is complete when its last kernel is.
-enum { kChainLead = 1, kChainFollow = 2 };
+// earlier work has returned, so X, Y and the residual are complete when a
+// follower starts.  griddepcontrol.wait makes them visible to the grid that
+// waited and says nothing of grids that start behind its trigger, so the lead
+// passes them on: behind its wait it raises `chain_flag` (release at device
+// scope), and a follower starts early only where it sees the flag raised
+// (acquire, and a proxy fence before its bulk copies); else it waits like any
+// other product.  The last follower lowers the flag at its end, when every
+// kernel of the chain is complete.
+// A follower's epilogue waits for the kernel before it where it may share memory
+// with that (split ranges' partials, the gate's values), else only at its end,
+// so the chain is complete when its last kernel is.
+enum { kChainLead = 1, kChainFollow = 2, kChainLast = 4 };
 // whether launch_hybrid_gemm / launch_fp8_gemm run this product on such a kernel
 bool hybrid_chains(const GemmLaunch &g);
 // The gated pair in one launch of the one-band kernel, and whether that is
@@ -313,6 +321,7 @@ struct Fp8Launch {
     int epi_on = 0;          // as GemmLaunch
     Epilogue epi;
     int chain = 0, peers = 1;
+    uint32_t *chain_flag = nullptr;
 };
 cudaError_t launch_fp8_gemm(const Fp8Launch &g, cudaStream_t stream);
 // whether launch_fp8_gemm runs the two-SM kernel for this product

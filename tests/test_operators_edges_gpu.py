@@ -59,3 +59,56 @@ def test_a_norm_that_is_off_ignores_its_parameters(P, gen, M, C):
     for clean, left in (((none, rms), (stray, rms)), ((rms, none), (rms, stray)), ((none, none), (stray, stray))):
         for got, want in zip(run(*left), run(*clean)):
             assert torch.equal(got, want)
+
+
+# --------------------------------- members side by side and their late inputs
+@pytest.mark.parametrize("kind", ["2:4", "4:8", "fp8"])
+@pytest.mark.parametrize("M", [20, 100, 300])
+def test_members_side_by_side_read_what_was_just_written(P, gen, kind, M):
+    # X, its scales, the residuals and the biases are all rewritten by the
+    # kernels right before the group, with other values in every pass
+    N, K = 384, 640
+    ws = [Weight(P, gen, n, K, kind) for n in (N, 128, N)]
+    packed = [w.packed for w in ws]
+    sets = []
+    for _ in range(3):
+        q, s = quantize(randn(gen, M, K))
+        sets.append({"x": q.view(torch.uint8) if kind == "fp8" else randn(gen, M, K, dtype=BF), "s": s,
+                     "r": randn(gen, M, N, dtype=BF), "t": randn(gen, M, N), "b": randn(gen, N)})
+    live = {k: torch.empty_like(v) for k, v in sets[0].items()}
+
+    def group(d):
+        return P.patch_hybrid_linear_group(packed, d["x"], x_scales=d["s"] if kind == "fp8" else None,
+                                           activation="silu", residuals=[d["r"], None, d["t"]], biases=[None, None, d["b"]])
+
+    want = []
+    for d in sets:
+        torch.cuda.synchronize()
+        want.append([y.clone() for y in group(d)])
+        torch.cuda.synchronize()
+    pick = torch.zeros(1, dtype=torch.long, device="cuda")
+    stacked = {k: torch.stack([d[k] for d in sets]) for k in live}
+
+    def step():
+        for k, v in live.items():
+            torch.index_select(stacked[k], 0, pick, out=v.unsqueeze(0))
+        # the last kernel before the group writes a residual: 0.5 * (2 r), exactly r
+        P.patch_block_norm(2 * live["r"], scale=0.5, out_h=live["r"])
+        return group(live)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for k in range(30):
+        pick.fill_(k % 3)
+        graph.replay()
+        pick.fill_((k + 1) % 3)
+        eager = step()
+        torch.cuda.synchronize()
+        for i, got in ((k % 3, captured), ((k + 1) % 3, eager)):
+            for y, y1 in zip(got, want[i]):
+                assert torch.equal(y, y1)
+    for w in packed:
+        assert P.patch_get_status(w) == 0
