@@ -77,17 +77,22 @@ const void *vector(const at::Tensor *t, int64_t n, c10::Device dev, const char *
     return t->const_data_ptr();
 }
 
-// address and row stride of an optional [M, C] tensor of contiguous rows
+// row stride of an [M, C] tensor of contiguous rows
+template <class TypeOk>
+int64_t row_step(const at::Tensor &t, int64_t M, int64_t C, c10::Device dev, const char *name, const TypeOk &type_ok) {
+    if (t.device() != dev || t.dim() != 2 || t.size(0) != M || t.size(1) != C || !type_ok(t))
+        refuse(name, " must be [", M, ", ", C, "] of its type on ", dev);
+    const int64_t step = M <= 1 ? C : t.stride(0);
+    if ((C > 1 && t.stride(1) != 1) || step < C) refuse(name, " must have contiguous rows that do not overlap");
+    return step;
+}
+
+// address and row stride of an optional input of that form
 template <class TypeOk>
 const void *rows(const at::Tensor *t, int64_t M, int64_t C, c10::Device dev, const char *name, int64_t *step,
                  const TypeOk &type_ok) {
-    *step = 0;
-    if (!t) return nullptr;
-    if (t->device() != dev || t->dim() != 2 || t->size(0) != M || t->size(1) != C || !type_ok(*t))
-        refuse(name, " must be [", M, ", ", C, "] of its type on ", dev);
-    *step = M <= 1 ? C : t->stride(0);
-    if ((C > 1 && t->stride(1) != 1) || *step < C) refuse(name, " must have contiguous rows that do not overlap");
-    return t->const_data_ptr();
+    *step = t ? row_step(*t, M, C, dev, name, type_ok) : 0;
+    return t ? t->const_data_ptr() : nullptr;
 }
 
 // A new tensor, without at::empty's way through the dispatcher (0.3 to 0.5 us of
@@ -96,11 +101,14 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
     return at::detail::empty_cuda(sizes, type, dev, std::nullopt);
 }
 
-// The output of a call: the caller's (checked), or a new tensor in `fresh`.
+// The output of a call: the caller's (checked), or a new tensor in `fresh`.  A
+// tensor that still shares its storage with a lazy clone gets its own here, so
+// outputs come before the addresses of inputs, which may be the same tensor.
 PyObject *output(PyObject *given, int64_t M, int64_t C, at::ScalarType type, c10::Device dev, const char *name,
                  at::Tensor *fresh, void **ptr, int64_t *step) {
     if (const at::Tensor *t = tensor(given, name)) {
-        *ptr = const_cast<void *>(rows(t, M, C, dev, name, step, [type](const at::Tensor &x) { return x.scalar_type() == type; }));
+        *step = row_step(*t, M, C, dev, name, [type](const at::Tensor &x) { return x.scalar_type() == type; });
+        *ptr = t->mutable_data_ptr();
         Py_INCREF(given);
         return given;
     }
@@ -131,18 +139,20 @@ Packed packed(PyObject *info) {
 struct Input {
     c10::Device dev = c10::Device(c10::kCUDA, 0);
     int64_t M;
-    const void *x;
-    const float *scales = nullptr;
+    const at::Tensor *X, *x_scales;
+    const void *x() const { return X->const_data_ptr(); }
+    const float *scales() const { return x_scales ? x_scales->const_data_ptr<float>() : nullptr; }
 };
 Input input(const Packed *ps, Py_ssize_t count, PyObject *X_o, PyObject *scales_o) {
     const at::Tensor *X = tensor(X_o, "X"), *sx = tensor(scales_o, "x_scales");
     Input in;
+    in.X = X;
+    in.x_scales = sx;
     in.dev = device_of(X, "X");
     if (X->dim() != 2 || !X->is_contiguous()) refuse("X must be a contiguous [M, K] tensor");
     in.M = X->size(0);
     for (Py_ssize_t i = 0; i < count; ++i)
         if (X->size(1) != ps[i].K) refuse("X has ", X->size(1), " columns, the packed weight ", ps[i].K);
-    in.x = X->const_data_ptr();
     if (!sx) {
         if (X->scalar_type() != at::kBFloat16)
             refuse("X has dtype ", X->scalar_type(), ", expected bfloat16 (or e4m3 codes with x_scales)");
@@ -155,7 +165,6 @@ Input input(const Packed *ps, Py_ssize_t count, PyObject *X_o, PyObject *scales_
     if (sx->device() != in.dev || sx->scalar_type() != at::kFloat || sx->dim() != 1 || sx->size(0) != in.M ||
         !sx->is_contiguous())
         refuse("x_scales must be a contiguous fp32 vector of ", in.M, " on ", in.dev);
-    in.scales = sx->const_data_ptr<float>();
     return in;
 }
 
@@ -213,6 +222,9 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *ys[kMaxGroup];
     at::Tensor fresh;
     Results out(count);
+    for (Py_ssize_t i = 0; i < count; ++i)
+        PyList_SET_ITEM(out.list, i, output(item(a[7], i, count, "outs"), in.M, ps[i].N, type, in.dev, "out", &fresh,
+                                            &ys[i], &epis[i].y_stride));
     for (Py_ssize_t i = 0; i < count; ++i) {
         const at::Tensor *bias = tensor(item(a[3], i, count, "biases"), "bias");
         const at::Tensor *res = tensor(item(a[6], i, count, "residuals"), "residual");
@@ -223,12 +235,10 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         e.activation = act;
         e.bias_is_fp32 = is_fp32(bias);
         e.residual_is_fp32 = is_fp32(res);
-        PyList_SET_ITEM(out.list, i, output(item(a[7], i, count, "outs"), in.M, ps[i].N, type, in.dev, "out", &fresh,
-                                            &ys[i], &e.y_stride));
     }
     void *stream = current_stream(in.dev);
     const patch_status st = without_gil([&] {
-        return g_linear(handles, static_cast<int32_t>(count), in.x, in.scales, in.M, ys, fp32, epis, stream);
+        return g_linear(handles, static_cast<int32_t>(count), in.x(), in.scales(), in.M, ys, fp32, epis, stream);
     });
     return st == PATCH_OK ? out.give() : PyLong_FromLong(st);
     END_HANDLE_TH_ERRORS
@@ -247,14 +257,14 @@ PyObject *gated(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int32_t act = static_cast<int32_t>(PyLong_AsLong(a[6]));
     const bool fp32 = PyObject_IsTrue(a[8]) == 1;
     if (PyErr_Occurred()) throw python_error();
-    const void *bgp = vector(bg, N, in.dev, "bias_gate"), *bup = vector(bu, N, in.dev, "bias_up");
     at::Tensor fresh;
     void *y;
     int64_t step;
     THPObjectPtr out(output(a[7], in.M, N, fp32 ? at::kFloat : at::kBFloat16, in.dev, "out", &fresh, &y, &step));
+    const void *bgp = vector(bg, N, in.dev, "bias_gate"), *bup = vector(bu, N, in.dev, "bias_up");
     void *stream = current_stream(in.dev);
     const patch_status st = without_gil([&] {
-        return g_gated(ps[0].handle, ps[1].handle, in.x, in.scales, in.M, y, step, fp32, bgp, bup,
+        return g_gated(ps[0].handle, ps[1].handle, in.x(), in.scales(), in.M, y, step, fp32, bgp, bup,
                        is_fp32(bg) || is_fp32(bu), act, stream);
     });
     return st == PATCH_OK ? out.release() : PyLong_FromLong(st);
@@ -293,28 +303,11 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (branch->dim() != 2) refuse("branch must be [M, C]");
     const int64_t M = branch->size(0), C = branch->size(1);
     patch_block_norm_args p = {};
-    p.branch = rows(branch, M, C, dev, "branch", &p.branch_stride, is_real);
-    p.residual = rows(res, M, C, dev, "residual", &p.residual_stride, is_real);
-    p.gate_tokens = 1;
-    if (gate) {
-        const int64_t R = gate->dim() == 2 ? gate->size(0) : 1;
-        if (R < 1 || M % R != 0) refuse("gate has ", R, " rows, which do not divide ", M, " tokens");
-        if (gate->dim() == 2)
-            p.gate = rows(gate, R, C, dev, "gate", &p.gate_stride, is_real);
-        else
-            p.gate = vector(gate, C, dev, "gate");
-        p.gate_tokens = M / R > 1 ? M / R : 1;
-    }
     p.scale = static_cast<float>(PyFloat_AsDouble(a[3]));
-    p.post = norm_spec(a[4], C, dev, "post");
-    p.pre = norm_spec(a[5], C, dev, "pre");
     p.z_type = static_cast<int32_t>(PyLong_AsLong(a[6]));
     const bool want_h = PyObject_IsTrue(a[7]) == 1;
     p.h_is_fp32 = PyObject_IsTrue(a[8]) == 1;
     if (PyErr_Occurred()) throw python_error();
-    p.branch_is_fp32 = is_fp32(branch);
-    p.residual_is_fp32 = is_fp32(res);
-    p.gate_is_fp32 = is_fp32(gate);
     at::Tensor fresh;
     THPObjectPtr h, z, scales;
     if (want_h)
@@ -333,6 +326,23 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else if (a[10] != Py_None) {
         refuse("out_z without a pre norm");
     }
+    p.branch = rows(branch, M, C, dev, "branch", &p.branch_stride, is_real);
+    p.residual = rows(res, M, C, dev, "residual", &p.residual_stride, is_real);
+    p.gate_tokens = 1;
+    if (gate) {
+        const int64_t R = gate->dim() == 2 ? gate->size(0) : 1;
+        if (R < 1 || M % R != 0) refuse("gate has ", R, " rows, which do not divide ", M, " tokens");
+        if (gate->dim() == 2)
+            p.gate = rows(gate, R, C, dev, "gate", &p.gate_stride, is_real);
+        else
+            p.gate = vector(gate, C, dev, "gate");
+        p.gate_tokens = M / R > 1 ? M / R : 1;
+    }
+    p.post = norm_spec(a[4], C, dev, "post");
+    p.pre = norm_spec(a[5], C, dev, "pre");
+    p.branch_is_fp32 = is_fp32(branch);
+    p.residual_is_fp32 = is_fp32(res);
+    p.gate_is_fp32 = is_fp32(gate);
     void *stream = current_stream(dev);
     const patch_status st = without_gil([&] { return g_norm(&p, M, C, stream); });
     if (st != PATCH_OK) return PyLong_FromLong(st);

@@ -61,6 +61,46 @@ def test_a_norm_that_is_off_ignores_its_parameters(P, gen, M, C):
             assert torch.equal(got, want)
 
 
+# ------------------------------------------- outputs that share their storage
+def test_an_output_that_is_a_lazy_clone_leaves_its_origin_alone(P, gen):
+    M, N = 40, 256
+    wg, wu = Weight(P, gen, N, 256), Weight(P, gen, N, 256)
+    x, res = randn(gen, M, 256, dtype=BF), randn(gen, M, N, dtype=BF)
+    pre = ("rms", None, None, 1e-5)
+
+    def fresh(origin):
+        return torch._lazy_clone(origin), origin.clone()
+
+    calls = [
+        (lambda o: P.patch_hybrid_linear(wg.packed, x, residual=res, out=o),
+         lambda: P.patch_hybrid_linear(wg.packed, x, residual=res)),
+        (lambda o: P.patch_hybrid_gated(wg.packed, wu.packed, x, out=o),
+         lambda: P.patch_hybrid_gated(wg.packed, wu.packed, x)),
+        (lambda o: P.patch_hybrid_linear_group([wg.packed, wu.packed], x, outs=[None, o])[1],
+         lambda: P.patch_hybrid_linear_group([wg.packed, wu.packed], x)[1]),
+        (lambda o: P.patch_block_norm(res, pre=pre, out_h=o)["h"], lambda: P.patch_block_norm(res, pre=pre)["h"]),
+        (lambda o: P.patch_block_norm(res, pre=pre, out_z=o)["z"], lambda: P.patch_block_norm(res, pre=pre)["z"]),
+    ]
+    for into, plain in calls:
+        origin = torch.zeros(M, N, dtype=BF, device="cuda")
+        out, keep = fresh(origin)
+        got, want = into(out), plain()
+        assert torch.equal(got, want) and torch.equal(out, want)
+        assert torch.equal(origin, keep)
+
+
+def test_an_in_place_update_of_a_lazy_clone(P, gen):
+    M, N = 40, 256
+    w = Weight(P, gen, N, 256)
+    x, origin = randn(gen, M, 256, dtype=BF), randn(gen, M, N, dtype=BF)
+    keep, stream = origin.clone(), torch._lazy_clone(origin)
+    P.patch_hybrid_linear(w.packed, x, residual=stream, out=stream)
+    assert torch.equal(stream, P.patch_hybrid_linear(w.packed, x, residual=keep)) and torch.equal(origin, keep)
+    stream = torch._lazy_clone(origin)
+    P.patch_block_norm(stream, residual=keep, out_h=stream)
+    assert torch.equal(stream, P.patch_block_norm(keep, residual=keep)["h"]) and torch.equal(origin, keep)
+
+
 # --------------------------------- members side by side and their late inputs
 @pytest.mark.parametrize("kind", ["2:4", "4:8", "fp8"])
 @pytest.mark.parametrize("M", [20, 100, 300])
