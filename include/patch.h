@@ -501,8 +501,9 @@ typedef struct {
  *   Y         [M] rows of N, y_stride (>= N) apart: bf16, or fp32
  *             (y_is_fp32 = 1).  Elements behind a row's N are left as they
  *             were.  Y may be the residual itself (same address, stride and
- *             type: the update is then in place); it must not overlap X, the
- *             bias or the residual in any other way.
+ *             type: the update is then in place); it must share no other byte
+ *             with X, its scales, a bias or a residual (rows between another
+ *             tensor's rows share none).
  *   epi       NULL = no bias, no residual, alpha 1, no activation.
  *
  * Stream-ordered; never waits for the device; may be captured into a CUDA
@@ -510,8 +511,8 @@ typedef struct {
  * concurrently (the rule of patch_hybrid_gemm), graphs that hold them
  * included.  Errors: INVALID_ARG (null or misaligned pointers, a stride below
  * N, an activation outside the list, x_scales on a handle that is not FP8, a
- * handle of another device, Y at X's address, or at the residual's with
- * another stride or type), OOM, CUDA.
+ * handle of another device, a Y that overlaps an input otherwise than in
+ * place), OOM, CUDA.
  */
 patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const float *x_scales,
                                  int64_t M, void *Y, int32_t y_is_fp32, const patch_epilogue *epi,
@@ -526,8 +527,8 @@ patch_status patch_hybrid_linear(const patch_packed *Wp, const void *X, const fl
  *   epis   host array of count epilogues, or NULL for none.
  * Every member's arguments are checked before anything is enqueued.  A
  * handle may appear more than once.  The members run in no order: an output
- * must overlap no other output and no other member's residual (INVALID_ARG
- * where one starts at the address of another).
+ * that overlaps another output, or another member's residual or bias, is
+ * INVALID_ARG.
  */
 patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t count, const void *X,
                                        const float *x_scales, int64_t M, void *const *Ys,
@@ -539,7 +540,7 @@ patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t c
  *
  *   Wgate, Wup  handles of the same N and K (any kinds), current device.
  *   X, x_scales, M  as patch_hybrid_linear (x_scales: both handles FP8).
- *   Y           [M] rows of N, y_stride (0 = N) apart; must not overlap X.
+ *   Y           [M] rows of N, y_stride (0 = N) apart; overlaps no input.
  *   bias_gate, bias_up  [N] each or NULL; fp32 when bias_is_fp32, else bf16.
  *
  * Notes and errors as patch_hybrid_linear; INVALID_ARG also for handles of
@@ -604,11 +605,11 @@ typedef struct {
  *      fp32 one on 32, the codes' on 8.
  *
  * h and z may each be the residual or the branch itself, not both the same one
- * (same address, stride and type); no other overlap.  Stream-ordered, no
+ * (same address, stride and type); an output overlaps nothing else.  Stream-ordered, no
  * scratch, no allocation.  Errors: INVALID_ARG (null branch, neither h nor z,
  * a stride below C, unknown kinds or types, eps negative or not a number,
- * misaligned pointers, z without z_type or z_scales where E4M3, an output at
- * an input's address with another stride or type), UNSUPPORTED (C above 32768,
+ * misaligned pointers, z without z_type or z_scales where E4M3, an output that
+ * overlaps another tensor otherwise than in place), UNSUPPORTED (C above 32768,
  * not sm_100), CUDA.
  */
 patch_status patch_block_norm(const patch_block_norm_args *args, int64_t M, int64_t C, void *stream);

@@ -15,6 +15,7 @@
 #include <new>
 #include <vector>
 
+#include "overlap.h"
 #include "patch.h"
 #include "patch_common.cuh"
 #include "patch_internal.h"
@@ -1224,6 +1225,22 @@ static bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintp
 static size_t real_bytes(int32_t is_fp32) { return is_fp32 ? 4 : 2; }
 static bool flag_ok(int32_t v) { return v == 0 || v == 1; }
 
+// the bytes of `rows` rows of n bf16 or fp32 values, `stride` values apart
+static patchk::ByteRows real_rows(const void *p, int64_t rows, int64_t stride, int64_t n, int32_t fp32) {
+    const int64_t b = static_cast<int64_t>(real_bytes(fp32));
+    // a stride beyond 2^59 values is no memory's: kept from overflowing
+    return {p, rows, std::min(stride, int64_t(1) << 59) * b, n * b};
+}
+static patchk::ByteRows y_rows(const patchk::Epilogue &e, const patch_packed *Wp, int64_t M, const void *Y,
+                               int32_t y_is_fp32) {
+    return real_rows(Y, M, e.ldy, Wp->shp.N, y_is_fp32);
+}
+static bool overlaps_input(const patchk::ByteRows &y, const patch_packed *Wp, const void *X, const float *x_scales,
+                           int64_t M) {
+    const int64_t bytes = M * Wp->shp.K * (x_scales ? 1 : 2);
+    return patchk::overlap(y, {X, 1, bytes, bytes}) || patchk::overlap(y, real_rows(x_scales, 1, M, M, 1));
+}
+
 // X, the handles and M of the calls below; the handles' device must be current.
 static patch_status check_products(const patch_packed *const *Wps, int32_t count, const void *X,
                                    const float *x_scales, int64_t M) {
@@ -1344,14 +1361,22 @@ patch_status patch_hybrid_linear_group(const patch_packed *const *Wps, int32_t c
         st = check_epilogue(epis ? epis + i : nullptr, Wps[i]->shp.N, M, Ys[i], y_is_fp32, &es[i]);
         if (st != PATCH_OK) return st;
     }
-    // the members run in no order: none may write what another writes or
-    // reads, and X is read to the end
-    for (int i = 0; i < count && M > 0; ++i)
-        if (Ys[i] == X) return PATCH_ERR_INVALID_ARG;
-    for (int i = 0; i < count && M > 0; ++i)
-        for (int j = 0; j < count; ++j)
-            if (i != j && (Ys[i] == Ys[j] || Ys[i] == es[j].residual)) return PATCH_ERR_INVALID_ARG;
     if (M == 0) return PATCH_OK;
+    // X is read to the end, and the members run in no order: none may write
+    // what another writes or reads
+    for (int i = 0; i < count; ++i) {
+        const patchk::ByteRows y = y_rows(es[i], Wps[i], M, Ys[i], y_is_fp32);
+        if (overlaps_input(y, Wps[0], X, x_scales, M)) return PATCH_ERR_INVALID_ARG;
+        for (int j = 0; j < count; ++j) {
+            const int64_t N = Wps[j]->shp.N;
+            if (j > i && patchk::overlap(y, y_rows(es[j], Wps[j], M, Ys[j], y_is_fp32))) return PATCH_ERR_INVALID_ARG;
+            // its own residual may be the output itself (check_epilogue: then wholly)
+            if ((i != j || Ys[i] != es[j].residual) &&
+                patchk::overlap(y, real_rows(es[j].residual, M, es[j].ldr, N, es[j].res_fp32)))
+                return PATCH_ERR_INVALID_ARG;
+            if (patchk::overlap(y, real_rows(es[j].bias, 1, N, N, es[j].bias_fp32))) return PATCH_ERR_INVALID_ARG;
+        }
+    }
     return no_throw([&] {
         return products(Wps, count, X, x_scales, M, Ys, y_is_fp32, es, static_cast<cudaStream_t>(stream_v));
     });
@@ -1376,7 +1401,11 @@ patch_status patch_hybrid_gated(const patch_packed *Wgate, const patch_packed *W
     if (st != PATCH_OK) return st;
     if (!aligned_to(bias_up, real_bytes(bias_is_fp32))) return PATCH_ERR_INVALID_ARG;
     if (M == 0) return PATCH_OK;
-    if (Y == X) return PATCH_ERR_INVALID_ARG;
+    const int64_t N = Wgate->shp.N;
+    const patchk::ByteRows y = y_rows(e, Wgate, M, Y, y_is_fp32);
+    if (overlaps_input(y, Wgate, X, x_scales, M) || patchk::overlap(y, real_rows(bias_gate, 1, N, N, bias_is_fp32)) ||
+        patchk::overlap(y, real_rows(bias_up, 1, N, N, bias_is_fp32)))
+        return PATCH_ERR_INVALID_ARG;
     patchk::Epilogue up;
     up.bias = bias_up;
     up.bias_fp32 = bias_is_fp32;
@@ -1423,6 +1452,7 @@ patch_status patch_block_norm(const patch_block_norm_args *a, int64_t M, int64_t
         (!e4m3 && !aligned_to(a->z, real_bytes(a->z_type == PATCH_Z_FP32))) || !aligned_to(a->z_scales, 4))
         return PATCH_ERR_INVALID_ARG;
     // in place: a thread writes the elements it read, so both must coincide
+    // (any other overlap is found below)
     const int32_t z_fp32 = a->z_type == PATCH_Z_FP32;
     auto clash = [](const void *out, int64_t os, int32_t of, const void *in, int64_t is, int32_t inf) {
         return out && out == in && (os != is || of != inf);
@@ -1438,6 +1468,27 @@ patch_status patch_block_norm(const patch_block_norm_args *a, int64_t M, int64_t
     if (!a->branch || (!a->h && a->z_type == PATCH_Z_NONE) || (a->z_type != PATCH_Z_NONE && !a->z) ||
         (a->z && a->z_type == PATCH_Z_NONE) || (e4m3 && !a->z_scales))
         return PATCH_ERR_INVALID_ARG;
+    const patchk::NormSpec post = norm_spec(a->post), pre = norm_spec(a->pre);
+    const int64_t gates = a->gate ? (M - 1) / a->gate_tokens + 1 : 0;
+    const patchk::ByteRows outs[3] = {
+        real_rows(a->h, M, p.h_stride, C, a->h_is_fp32),
+        e4m3 ? patchk::ByteRows{a->z, M, p.z_stride, C} : real_rows(a->z, M, p.z_stride, C, z_fp32),
+        e4m3 ? real_rows(a->z_scales, 1, M, M, 1) : patchk::ByteRows()};
+    const patchk::ByteRows ins[7] = {real_rows(a->branch, M, p.branch_stride, C, a->branch_is_fp32),
+                                     real_rows(a->residual, M, p.residual_stride, C, a->residual_is_fp32),
+                                     real_rows(a->gate, gates, p.gate_stride, C, a->gate_is_fp32),
+                                     real_rows(post.weight, 1, C, C, post.fp32),
+                                     real_rows(post.bias, 1, C, C, post.fp32),
+                                     real_rows(pre.weight, 1, C, C, pre.fp32),
+                                     real_rows(pre.bias, 1, C, C, pre.fp32)};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 3; ++j)
+            if (patchk::overlap(outs[i], outs[j])) return PATCH_ERR_INVALID_ARG;
+        for (int j = 0; j < 7; ++j) {
+            const bool in_place = i < 2 && j < 2 && outs[i].at == ins[j].at;
+            if (!in_place && patchk::overlap(outs[i], ins[j])) return PATCH_ERR_INVALID_ARG;
+        }
+    }
     const patch_status st = check_device(&p.num_sms);
     if (st != PATCH_OK) return st;
     p.branch = a->branch;
@@ -1448,8 +1499,8 @@ patch_status patch_block_norm(const patch_block_norm_args *a, int64_t M, int64_t
     p.z_scales = a->z_scales;
     p.gate_tokens = a->gate ? a->gate_tokens : 1;
     p.M = M;
-    p.post = norm_spec(a->post);
-    p.pre = norm_spec(a->pre);
+    p.post = post;
+    p.pre = pre;
     p.scale = a->scale;
     p.C = static_cast<int>(C);
     p.branch_fp32 = a->branch_is_fp32;

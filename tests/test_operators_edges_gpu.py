@@ -101,6 +101,39 @@ def test_an_in_place_update_of_a_lazy_clone(P, gen):
     assert torch.equal(stream, P.patch_block_norm(keep, residual=keep)["h"]) and torch.equal(origin, keep)
 
 
+# --------------------------------------------- overlapping tensors are refused
+def test_overlapping_outputs_and_inputs_are_refused(P, gen):
+    # refused before anything is enqueued: every tensor keeps its bits
+    N, K, M = 256, 512, 20
+    packed = [Weight(P, gen, N, K).packed for _ in range(2)]
+    big = randn(gen, M + 2, 1024, dtype=BF)
+    keep = big.clone()
+    x = randn(gen, M, K, dtype=BF)
+    rows = lambda c, r=0: big[r:r + M, c:c + N]  # noqa: E731
+    flat = big.view(-1)
+    at = lambda i, n, m: flat[i:i + m * n].view(m, n)  # noqa: E731
+    ok = P.patch_hybrid_linear_group(packed, x, outs=[rows(0), rows(256)], residuals=[rows(512), rows(768)])
+    want = P.patch_hybrid_linear_group(packed, x, residuals=[keep[:M, 512:768], keep[:M, 768:]])
+    assert all(torch.equal(a, b) for a, b in zip(ok, want))
+    big.copy_(keep)
+    refused = [
+        lambda: P.patch_hybrid_linear_group(packed, x, outs=[rows(0), rows(128)]),
+        lambda: P.patch_hybrid_linear_group(packed, x, outs=[rows(0), rows(0, 1)]),
+        lambda: P.patch_hybrid_linear_group(packed, x, outs=[rows(0), rows(512)], residuals=[None, rows(255)]),
+        lambda: P.patch_hybrid_linear(packed[0], x, out=rows(0), residual=rows(8)),
+        lambda: P.patch_hybrid_linear(packed[0], x, out=rows(0), residual=rows(0, 1)),
+        lambda: P.patch_hybrid_linear(packed[0], x, out=rows(0), bias=flat[64:64 + N]),
+        lambda: P.patch_hybrid_linear(packed[0], at(1024, K, M), out=at(1024 + K, N, M)),
+        lambda: P.patch_hybrid_gated(packed[0], packed[1], at(0, K, M), out=at(K, N, M)),
+        lambda: P.patch_hybrid_gated(packed[0], packed[1], x, out=rows(256), bias_up=flat[400:400 + N]),
+    ]
+    for call in refused:
+        with pytest.raises(P.PatchError):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(big, keep)
+
+
 # --------------------------------- members side by side and their late inputs
 @pytest.mark.parametrize("kind", ["2:4", "4:8", "fp8"])
 @pytest.mark.parametrize("M", [20, 100, 300])
