@@ -22,13 +22,20 @@ enum EpiMode { kEpiPlain = 0, kEpiLinear = 1, kEpiGated = 2 };
 
 // The activations, through CUDA's own math functions.
 __device__ __forceinline__ float act_relu(float v) { return v < 0.0f ? 0.0f : v; }  // NaN stays NaN
+// off by 3 |v| 2^-24: far below zero 1 + erf, and so the result, keeps few digits
+// (erfcf keeps them: 4096 tokens, 4096x1024 45 -> 62 us)
 __device__ __forceinline__ float act_gelu(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678f)); }
-// x / (1 + exp(-y)) by the hardware's exponential and reciprocal: off by at most
-// about 2^-21 + 2^-24 |y| of the result, against 2^-9 for a bf16 output.  Eight
-// warps finish an accumulator, so a short K is bound by these instructions
-// (FP8, 2478 tokens, 7168x256 gated: 66 us, 77 with tanhf).
+// x / (1 + exp(-y)) by the hardware's exponential and reciprocal.  __expf is
+// documented at 2 + floor(|1.173 y|) ulp and __fdividef at 2: with the sum's
+// rounding (10 + 2.4 |y|) 2^-24 of the result (0 below y = -87.3, where the result
+// is under 2^-118).  A bf16 output rounds by 2^-9; an fp32 output's sums are off
+// by more than that from some tens of terms on (2^-23 for every 16 added).
+// Eight warps finish an accumulator, so a short K is bound by these instructions
+// (FP8, 2478 tokens, 7168x256 gated: 66 us, 77 with tanhf; 4096 tokens, 4096x1024
+// gated, fp32 output: 53 us, 81 by expf and a full division, 62 by an exponential
+// with its argument's rounding corrected).
 __device__ __forceinline__ float over_one_plus_exp(float x, float y) { return __fdividef(x, 1.0f + __expf(-y)); }
-// (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u))
+// (1 + tanh(u)) / 2 = 1 / (1 + exp(-y)), y = 2 u; y's own roundings add 5 |y| 2^-24
 __device__ __forceinline__ float act_gelu_tanh(float v) {
     return over_one_plus_exp(v, v * fmaf(0.07135481f * v, v, 1.59576912f));
 }

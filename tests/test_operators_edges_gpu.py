@@ -3,8 +3,8 @@ switched off with pointers left in them, outputs that share their storage,
 overlapping tensors, groups whose inputs were written just before, and the
 accuracy of the activations in fp32 outputs.
 
-Tolerances count roundings, u = 2^-24 (half an fp32 step), with CUDA's
-documented error bounds of expf (2 ulp = 4 u) and normcdff (5 ulp = 10 u).
+Tolerances count roundings, u = 2^-24 (half an fp32 step), with the documented
+error bounds of the instructions and functions used.
 """
 import ctypes
 import math
@@ -99,6 +99,61 @@ def test_an_in_place_update_of_a_lazy_clone(P, gen):
     stream = torch._lazy_clone(origin)
     P.patch_block_norm(stream, residual=keep, out_h=stream)
     assert torch.equal(stream, P.patch_block_norm(keep, residual=keep)["h"]) and torch.equal(origin, keep)
+
+
+# ----------------------------------------------- activations in fp32 outputs
+def identity(P, n, nm=(2, 4)):
+    """A packed n x n identity of dense tiles: every sum is one value of X, exactly."""
+    w = torch.eye(n, dtype=BF, device="cuda")
+    return P.patch_pack(w, torch.full((n, n // 32), 0x44444444, dtype=torch.int32, device="cuda"),
+                        torch.zeros(1, dtype=torch.int32, device="cuda"), tile_n=128, tile_k=128, nm=nm)
+
+
+def value_and_bound(v, kind):
+    """act(v) in 64 bits and the error that the header states, from v (exact).
+
+    silu: e = __expf(-v) is off by 2 + floor(|1.173 v|) ulp of 2 u, 1 + e by u,
+      __fdividef by 2 ulp (4 u): (9 + 2.35 |v|) u; a quotient over 2^126 may be 0.
+    tanh GELU: the same behind y = v (c0 + c1 v^2), which has two rounded
+      constants and three roundings, 5 u |y| in the exponent.
+    GELU: erff is off by 2 ulp (2 u below 1), its argument by 2 u (worth 1 u: x
+      erf'(x) <= 0.49), 1 + erf by u: 4 u of 0.5 |v|, and one rounded product."""
+    if kind == "gelu":
+        want = 0.5 * v * torch.special.erfc(-v / math.sqrt(2.0))
+        return want, 3 * U * v.abs()
+    y = v if kind == "silu" else math.sqrt(8 / math.pi) * (v + 0.044715 * v ** 3)
+    want = v * torch.sigmoid(y)
+    return want, (10 + (2.4 if kind == "silu" else 7.4) * y.abs()) * U * want.abs() + 2.0 ** -118
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [1, 40, 100, 300])
+def test_activations_of_fp32_outputs(P, gen, kind, M):
+    n = 256
+    w = identity(P, n)
+    span = torch.linspace(-12, 12, M * n, device="cuda")[torch.randperm(M * n, generator=gen, device="cuda")]
+    x = span.to(BF).view(M, n)
+    v = x.double()
+    want, tol = value_and_bound(v, kind)
+    got = P.patch_hybrid_linear(w, x, activation=kind, out_fp32=True).double()
+    err = (got - want).abs()
+    assert (err <= tol).all(), (err / tol).max().item()
+    # the gated pair: the same value times the up projection's, one more rounding
+    got = P.patch_hybrid_gated(w, w, x, activation=kind, out_fp32=True).double()
+    err = (got - want * v).abs()
+    assert (err <= tol * v.abs() + 2 * U * (want * v).abs() + 2.0 ** -118).all()
+
+
+def test_activations_of_fp32_outputs_far_out(P):
+    # no infinity, NaN or early zero where an exponential over- or underflows
+    n = 256
+    w = identity(P, n)
+    for M in (2, 100, 300):
+        x = (torch.linspace(-100, 100, M * n, device="cuda")).to(BF).view(M, n)
+        for kind in ("silu", "gelu", "gelu_tanh"):
+            want, tol = value_and_bound(x.double(), kind)
+            got = P.patch_hybrid_linear(w, x, activation=kind, out_fp32=True).double()
+            assert ((got - want).abs() <= tol).all()
 
 
 # --------------------------------------------- overlapping tensors are refused
