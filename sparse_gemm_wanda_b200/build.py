@@ -45,12 +45,22 @@ def _stale(srcs, out) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_target() -> str:
+    """The PyTorch and Python that a binding is built against, and for."""
+    import sysconfig
+
+    import torch
+
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def _build_binding() -> None:
     """The CPython module over PyTorch tensors (csrc/torch_binding.cpp)."""
     import sysconfig
 
     import torch
 
+    target = binding_target()
     base = os.path.dirname(torch.__file__)
     include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
@@ -58,30 +68,44 @@ def _build_binding() -> None:
     tmp = BINDING_OUT + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", sysconfig.get_path("include"), "-I", INCLUDE, *[f"-isystem{p}" for p in include], BINDING_SRC,
+           f'-DPATCH_BUILT_FOR="{target}"', "-I", sysconfig.get_path("include"), "-I", INCLUDE, *[f"-isystem{p}" for p in include], BINDING_SRC,
            "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
            "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_OUT)
+    with open(_binding_stamp(), "w") as fh:
+        fh.write(target)
+
+
+def _binding_stamp() -> str:
+    return os.path.join(BUILD_DIR, "_patch_torch.txt")
 
 
 def _stale_binding() -> bool:
-    if not os.path.exists(BINDING_OUT):
+    if not os.path.exists(BINDING_OUT) or not os.path.exists(_binding_stamp()):
         return True
+    with open(_binding_stamp()) as fh:
+        if fh.read() != binding_target():
+            return True
     t = os.path.getmtime(BINDING_OUT)
     deps = [BINDING_SRC, os.path.join(INCLUDE, "patch.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Both, the CUDA library first: it needs no PyTorch."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    if force or _stale(srcs, OUT):
+        _build_library(srcs, verbose)
     if force or _stale_binding():
         _build_binding()
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    if not force and not _stale(srcs, OUT):
-        return OUT
-    os.makedirs(BUILD_DIR, exist_ok=True)
+    return OUT
+
+
+def _build_library(srcs, verbose: bool) -> None:
     cc = nvcc()
 
     def compile_one(src):
@@ -104,7 +128,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OUT)
-    return OUT
 
 
 if __name__ == "__main__":

@@ -385,4 +385,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_patch_torch", nullptr, -1, g_me
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__patch_torch(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__patch_torch(void) {
+    PyObject *m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "built_for", PATCH_BUILT_FOR) != 0) Py_CLEAR(m);
+    return m;
+}

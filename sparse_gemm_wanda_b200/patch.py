@@ -13,6 +13,8 @@ import os
 
 import torch
 
+from .build import binding_target
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpatch_b200.so")
 
@@ -515,6 +517,9 @@ def _load_native():
             spec.loader.exec_module(module)
         except ImportError as exc:
             raise PatchLibraryError(f"cannot load {path}: {exc}") from exc
+        if module.built_for != binding_target():
+            raise PatchLibraryError(f"{path} was built for {module.built_for}, this is {binding_target()}: "
+                                    "build it with `python -m sparse_gemm_wanda_b200.build`")
         module.bind(*[ctypes.cast(f, ctypes.c_void_p).value
                       for f in (lib.patch_hybrid_linear_group, lib.patch_hybrid_gated, lib.patch_block_norm)])
         _native = module

@@ -107,3 +107,54 @@ def test_block_norm_takes_neighbours_and_in_place(P, kw):
     # past every check of the arguments: the device is asked for, and missing
     norms = {k: P.PatchNorm(*v) for k, v in kw.items() if isinstance(v, tuple)}
     assert norm_status(P, 4, 64, **{**kw, **norms}) in (2, 3)
+
+
+# ------------------------------------------------------ building the native modules
+@pytest.fixture
+def fake_build(monkeypatch, tmp_path):
+    """The build module over a folder of its own; compilers that only leave their output file."""
+    from sparse_gemm_wanda_b200 import build
+    ran, fail = [], set()
+
+    def run(cmd, **_):
+        tool = os.path.basename(cmd[0])
+        ran.append(tool)
+        if tool not in fail:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, int(tool in fail), "", "no such header")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    monkeypatch.setattr(build, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
+    monkeypatch.setenv("CXX", "g++")
+    for name, leaf in (("OUT", "lib.so"), ("BINDING_OUT", "binding.so"), ("BUILD_DIR", "_build")):
+        monkeypatch.setattr(build, name, str(tmp_path / leaf))
+    return build, ran, fail
+
+
+def test_the_library_is_built_without_the_binding(fake_build):
+    build, ran, fail = fake_build
+    fail.add("g++")
+    with pytest.raises(RuntimeError, match="no such header"):
+        build.build()
+    assert os.path.exists(build.OUT) and not os.path.exists(build.BINDING_OUT)
+
+
+def test_a_binding_for_another_torch_is_rebuilt(fake_build, monkeypatch):
+    build, ran, _ = fake_build
+    build.build()
+    assert "nvcc" in ran and ran[-1] == "g++"
+    ran.clear()
+    build.build()
+    assert ran == []
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    build.build()
+    assert ran == ["g++"]
+    build.build()
+    assert ran == ["g++"]
+
+
+def test_a_binding_for_another_torch_is_not_loaded(P, monkeypatch):
+    monkeypatch.setattr(P, "_native", None)
+    monkeypatch.setattr(P, "binding_target", lambda: "torch 0.0.1, cpython-30")
+    with pytest.raises(P.PatchLibraryError, match="0.0.1"):
+        P.patch_block_norm(torch.zeros(2, 64, dtype=torch.bfloat16))
