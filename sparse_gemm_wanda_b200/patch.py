@@ -13,8 +13,6 @@ import os
 
 import torch
 
-from .build import binding_target
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpatch_b200.so")
 
@@ -517,6 +515,7 @@ def _load_native():
             spec.loader.exec_module(module)
         except ImportError as exc:
             raise PatchLibraryError(f"cannot load {path}: {exc}") from exc
+        from .build import binding_target  # here: `python -m sparse_gemm_wanda_b200.build` imports this package
         if module.built_for != binding_target():
             raise PatchLibraryError(f"{path} was built for {module.built_for}, this is {binding_target()}: "
                                     "build it with `python -m sparse_gemm_wanda_b200.build`")

@@ -154,7 +154,8 @@ def test_a_binding_for_another_torch_is_rebuilt(fake_build, monkeypatch):
 
 
 def test_a_binding_for_another_torch_is_not_loaded(P, monkeypatch):
+    from sparse_gemm_wanda_b200 import build
     monkeypatch.setattr(P, "_native", None)
-    monkeypatch.setattr(P, "binding_target", lambda: "torch 0.0.1, cpython-30")
+    monkeypatch.setattr(build, "binding_target", lambda: "torch 0.0.1, cpython-30")
     with pytest.raises(P.PatchLibraryError, match="0.0.1"):
         P.patch_block_norm(torch.zeros(2, 64, dtype=torch.bfloat16))
