@@ -409,8 +409,8 @@ __device__ __forceinline__ void copies_left() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The same for many rows of RMS norms without biases and at most a gate per
-// channel (the shapes of a prefill): the blocks stay, one to an SM, and every
+// The same for many all-bf16 rows of RMS norms without biases and at most a gate
+// per channel (the shapes of a prefill): the blocks stay, one to an SM, and every
 // team of threads runs down its rows with the next one on its way into shared
 // memory.  A thread copies exactly the bytes it will read, so a row needs no
 // barrier before its values are used, and no register waits for a value.
@@ -418,8 +418,8 @@ __device__ __forceinline__ void copies_left() {
 // multiplied once: per value that is one load and one product in place of two
 // or three loads, conversions and products.
 // Shared memory: [post C] [pre C] fp32, then [2][teams][planes][NV * threads]
-// of 16 bytes, a plane for the branch and one for the residual (two where fp32).
-template <class TY, int NV, int MAXT>
+// of 16 bytes, a plane for the branch and one for the residual.
+template <int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1)
 block_norm_stream_kernel(const __grid_constant__ BlockNormParams p, int threads) {
     extern __shared__ uint4 ring_raw[];
@@ -437,39 +437,30 @@ block_norm_stream_kernel(const __grid_constant__ BlockNormParams p, int threads)
     Team team{red + 64 * j, threads, t, 1 + j};
     const Place<true> at{t, threads, C};
     const int plane = NV * threads;
-    const int bp = TY::branch(p) ? 2 : 1, rp = p.residual ? (TY::residual(p) ? 2 : 1) : 0;
-    const int slot_stride = teams * (bp + rp) * plane;
-    const uint4 *mine = ring + j * (bp + rp) * plane + t;
+    const int planes = p.residual ? 2 : 1;
+    const int slot_stride = teams * planes * plane;
+    const uint4 *mine = ring + j * planes * plane + t;
     const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * teams + j;
 
     auto fetch = [&](int64_t m, int slot) {
         if (m < p.M) {
             const uint32_t dst = smem_u32(mine + slot * slot_stride);
-            const char *b = static_cast<const char *>(p.branch) + (m * p.branch_stride + t * 8) * (2 * bp);
-            const char *r = static_cast<const char *>(p.residual) + (m * p.residual_stride + t * 8) * (2 * rp);
+            const uint16_t *b = static_cast<const uint16_t *>(p.branch) + m * p.branch_stride + t * 8;
+            const uint16_t *r = static_cast<const uint16_t *>(p.residual) + m * p.residual_stride + t * 8;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (!at.has(i)) continue;
                 const uint32_t d = dst + 16u * static_cast<uint32_t>(i * threads);
-                const int o = i * threads * 16;  // bytes of bf16
-                copy16(d, b + o * bp);
-                if (bp == 2) copy16(d + 16u * plane, b + o * bp + 16);
-                if (rp >= 1) copy16(d + 16u * (bp * plane), r + o * rp);
-                if (rp == 2) copy16(d + 16u * ((bp + 1) * plane), r + o * rp + 16);
+                copy16(d, b + i * threads * 8);
+                if (p.residual) copy16(d + 16u * plane, r + i * threads * 8);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto take = [&](int slot, int from, int i, int fp32, float2(&f)[4]) {
-        const uint4 *q = mine + slot * slot_stride + from * plane + i * threads;
-        const uint4 a = q[0];
-        Raw r{{a.x, a.y, a.z, a.w, 0, 0, 0, 0}};
-        if (fp32) {
-            const uint4 b = q[plane];
-            r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
-        }
-        unpack8<true>(r, fp32, f);
+    auto take = [&](int slot, int from, int i, float2(&f)[4]) {
+        const uint4 a = mine[slot * slot_stride + from * plane + i * threads];
+        unpack8<true>(Raw{{a.x, a.y, a.z, a.w}}, 0, f);
     };
     // v *= the 8 weights of chunk i
     auto times = [&](const float *w, int i, float2(&v)[4]) {
@@ -493,11 +484,11 @@ block_norm_stream_kernel(const __grid_constant__ BlockNormParams p, int threads)
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
         if (has_a) {
             float a = p.scale;
-            if (p.post.weight) a *= load_real(p.post.weight, c, p.post.fp32);
-            if (p.gate) a *= load_real(p.gate, c, p.gate_fp32);
+            if (p.post.weight) a *= load_real(p.post.weight, c, 0);
+            if (p.gate) a *= load_real(p.gate, c, 0);
             wa[c] = a;
         }
-        if (has_b) wb[c] = load_real(p.pre.weight, c, p.pre.fp32);
+        if (has_b) wb[c] = load_real(p.pre.weight, c, 0);
     }
     __syncthreads();
     const float scale = has_a ? 1.0f : p.scale;
@@ -510,7 +501,7 @@ block_norm_stream_kernel(const __grid_constant__ BlockNormParams p, int threads)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (at.has(i)) {
-                take(slot, 0, i, TY::branch(p), v[i]);
+                take(slot, 0, i, v[i]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i][k] = both(0.0f);
@@ -524,14 +515,14 @@ block_norm_stream_kernel(const __grid_constant__ BlockNormParams p, int threads)
             if (has_a) times(wa, i, v[i]);
             if (p.residual) {
                 float2 r[4];
-                take(slot, bp, i, TY::residual(p), r);
+                take(slot, 1, i, r);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i][k] = fma2(both(f), v[i][k], r[k]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i][k] = mul2(v[i][k], both(f));
             }
-            if (p.h) store8(p.h, m * p.h_stride, at, i, TY::h(p), v[i]);
+            if (p.h) store8(p.h, m * p.h_stride, at, i, 0, v[i]);
         }
         slot ^= 1;
         if (p.z_type == kZNone) continue;
@@ -606,7 +597,7 @@ cudaError_t run_stream(const BlockNormParams &p, cudaStream_t stream) {
     int threads = 0, smem = 0;
     const int teams = stream_teams<NV, MAXT>(p, &threads, &smem);
     if (teams < 1) return cudaErrorInvalidValue;
-    const cudaError_t attr_err = allow_smem<block_norm_stream_kernel<AllBf16, NV, MAXT>>(kNormSmem);
+    const cudaError_t attr_err = allow_smem<block_norm_stream_kernel<NV, MAXT>>(kNormSmem);
     if (attr_err != cudaSuccess) return attr_err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(p.num_sms, (p.M + teams - 1) / teams)));
@@ -618,7 +609,7 @@ cudaError_t run_stream(const BlockNormParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, block_norm_stream_kernel<AllBf16, NV, MAXT>, p, threads);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, block_norm_stream_kernel<NV, MAXT>, p, threads);
     if (err == cudaSuccess) note_launches(1);
     return err;
 }
@@ -676,8 +667,11 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream) {
                    : run_types<AnyTypes, 2, 512, 2, true, false>(p, stream);
     // (1500 x 12000, a layer norm, 48.2 against 59.3; single accesses, whose
     // 1541 x 8585 takes 46.6 this way, keep four: 37.7)
-    if (any && vec) return run_types<AnyTypes, 2, 1024, 1, true, true>(p, stream);
-    return run<4, 512, 2, false>(p, vec, stream);
+    if (any)
+        return vec ? run_types<AnyTypes, 2, 1024, 1, true, true>(p, stream)
+                   : run_types<AnyTypes, 4, 512, 2, false, false>(p, stream);
+    return AllBf16::fit(p) ? run_types<AllBf16, 4, 512, 2, false, true>(p, stream)
+                           : run_types<Fp32Stream, 4, 512, 2, false, true>(p, stream);
 }
 
 }  // namespace patchk
