@@ -61,6 +61,31 @@ def test_a_norm_that_is_off_ignores_its_parameters(P, gen, M, C):
             assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("M,C", [(4096, 4096), (3001, 5120), (900, 16384)])
+def test_norms_of_many_rows_with_every_parameter_in_bf16(P, gen, M, C):
+    # the parts of the shared-memory ring: a gate with a weightless post norm
+    # and no pre norm, e4m3 output behind weights, no residual, z in fp32
+    bf = dict(dtype=BF)
+    b, r = randn(gen, M, C, **bf), randn(gen, M, C, **bf)
+    rms = lambda: ("rms", randn(gen, C, spread=0.2, **bf) + 1, None, 1e-5)  # noqa: E731
+    check_norm(P, b, r, gate=randn(gen, 1, C, **bf), post=("rms", None, None, 1e-5), pre=None)
+    check_norm(P, b, r, post=rms(), pre=rms(), z_type="e4m3")
+    check_norm(P, b, r, pre=rms(), z_type="e4m3")
+    check_norm(P, b, None, gate=randn(gen, C, **bf), post=rms(), pre=("rms", None, None, 1e-5), z_type="fp32")
+
+
+@pytest.mark.parametrize("M,C", [(64, 4096), (300, 1032), (33, 999), (4096, 4096)])
+def test_codes_behind_a_norm_are_the_rounded_quotients(P, gen, M, C):
+    # the codes are those of the normed fp32 row divided by its scale, bit for bit
+    for dtype in (BF, F32):
+        b, pre = randn(gen, M, C, dtype=dtype), ("rms", randn(gen, C, dtype=dtype), None, 1e-5)
+        z = P.patch_block_norm(b, pre=pre, z_type="fp32")["z"]
+        e = P.patch_block_norm(b, pre=pre, z_type="e4m3")
+        q, s = quantize(z)
+        assert torch.equal(e["scales"], s)
+        assert torch.equal(e["z"], q.view(torch.uint8))
+
+
 # ------------------------------------------- outputs that share their storage
 def test_an_output_that_is_a_lazy_clone_leaves_its_origin_alone(P, gen):
     M, N = 40, 256
