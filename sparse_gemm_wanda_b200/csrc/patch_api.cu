@@ -72,6 +72,17 @@ struct DevInfo {
     int major = 0, minor = 0, sms = 0;
 };
 
+// Host-side planning allocates; running out of host memory is an error of the
+// call, not an exception through the C boundary.
+template <class Call>
+patch_status no_throw(const Call &call) {
+    try {
+        return call();
+    } catch (...) {
+        return PATCH_ERR_OOM;
+    }
+}
+
 // Compute capability and SM count of the current device (queried once).
 patch_status check_device(int *num_sms) {
     static std::mutex mu;
@@ -79,7 +90,7 @@ patch_status check_device(int *num_sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PATCH_ERR_CUDA;
     DevInfo info;
-    {
+    const patch_status st = no_throw([&] {
         std::lock_guard<std::mutex> lock(mu);
         auto it = cache.find(dev);
         if (it != cache.end()) {
@@ -91,7 +102,9 @@ patch_status check_device(int *num_sms) {
                 return PATCH_ERR_CUDA;
             cache[dev] = info;
         }
-    }
+        return PATCH_OK;
+    });
+    if (st != PATCH_OK) return st;
     if (info.major != 10 || info.minor != 0) return PATCH_ERR_UNSUPPORTED;
     if (num_sms) *num_sms = info.sms;
     return PATCH_OK;
@@ -160,17 +173,6 @@ patch_status from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return PATCH_OK;
     if (e == cudaErrorMemoryAllocation) return PATCH_ERR_OOM;
     return PATCH_ERR_CUDA;
-}
-
-// Host-side planning allocates; running out of host memory is an error of the
-// call, not an exception through the C boundary.
-template <class Call>
-patch_status no_throw(const Call &call) {
-    try {
-        return call();
-    } catch (...) {
-        return PATCH_ERR_OOM;
-    }
 }
 
 // epi null: the plain product

@@ -265,3 +265,54 @@ def test_members_side_by_side_read_what_was_just_written(P, gen, kind, M):
                 assert torch.equal(y, y1)
     for w in packed:
         assert P.patch_get_status(w) == 0
+
+
+# ------------------------------------------------ exceptions at the C boundary
+def test_no_exception_leaves_the_first_call_out_of_host_memory(tmp_path):
+    # the first call of a process notes the device's properties, which allocates
+    import os
+    import subprocess
+    import sys
+    src = tmp_path / "shim.cpp"
+    src.write_text("""
+#include <cstdlib>
+#include <new>
+static thread_local int failing = 0;
+extern "C" void fail_new(int on) { failing = on; }
+static void *get(std::size_t n) {
+    void *p = failing ? nullptr : std::malloc(n ? n : 1);
+    if (!p) throw std::bad_alloc();
+    return p;
+}
+void *operator new(std::size_t n) { return get(n); }
+void *operator new[](std::size_t n) { return get(n); }
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete[](void *p) noexcept { std::free(p); }
+void operator delete(void *p, std::size_t) noexcept { std::free(p); }
+void operator delete[](void *p, std::size_t) noexcept { std::free(p); }
+""")
+    shim = str(tmp_path / "shim.so")
+    subprocess.run(["g++", "-O1", "-shared", "-fPIC", str(src), "-o", shim], check=True)
+    code = """
+import ctypes, sys, torch
+from sparse_gemm_wanda_b200 import patch as P
+shim, lib = ctypes.CDLL(sys.argv[1]), P.load_library()
+x = torch.randn(4, 64, device="cuda").bfloat16()
+h = torch.zeros_like(x)
+a = P.PatchBlockNormArgs()
+a.branch, a.h, a.scale = x.data_ptr(), h.data_ptr(), 1.0
+arg, M, C, stream, run = ctypes.byref(a), 4, 64, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), lib.patch_block_norm
+fail = shim.fail_new
+fail(1)
+status = run(arg, M, C, stream)
+fail(0)
+assert P.STATUS_NAMES[status] == "PATCH_ERR_OOM", status
+assert run(arg, M, C, stream) == 0
+torch.cuda.synchronize()
+assert torch.equal(x, h)
+print("returned")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code, shim], cwd=root, env={**os.environ, "LD_PRELOAD": shim},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "returned" in r.stdout, r.stderr[-2000:]
