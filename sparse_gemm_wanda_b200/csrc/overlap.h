@@ -7,19 +7,33 @@
 
 namespace patchk {
 
-// `count` rows of `width` bytes, `stride` >= `width` bytes apart.  No rows: nothing.
+// `count` rows of `width` bytes, `stride` >= `width` bytes apart, from `begin` up
+// to `end`.  Null, or no rows: nothing (begin = end).
 struct ByteRows {
-    const void *at = nullptr;
     int64_t count = 0, stride = 0, width = 0;
+    uintptr_t begin = 0, end = 0;
+    ByteRows() = default;
+    ByteRows(const void *at, int64_t count, int64_t stride, int64_t width)
+        : count(count), stride(stride), width(width), begin(reinterpret_cast<uintptr_t>(at)), end(begin) {
+        if (!at || count < 1 || width < 1) return;
+        // (128 bits: a stride may be any 64-bit number)
+        const __int128 last = static_cast<__int128>(count - 1) * stride + width + begin;
+        end = last > static_cast<__int128>(UINTPTR_MAX) ? UINTPTR_MAX : static_cast<uintptr_t>(last);
+    }
 };
 
-inline bool overlap(ByteRows a, ByteRows b) {
-    using wide = __int128;  // a stride may be any 64-bit number
-    if (!a.at || !b.at || a.count < 1 || b.count < 1 || a.width < 1 || b.width < 1) return false;
+inline bool rows_meet(ByteRows a, ByteRows b);
+
+// most pairs are apart as a whole
+inline bool overlap(const ByteRows &a, const ByteRows &b) {
+    return a.begin < b.end && b.begin < a.end && a.begin < a.end && b.begin < b.end && rows_meet(a, b);
+}
+
+// the rows of two sets whose ranges meet
+inline bool rows_meet(ByteRows a, ByteRows b) {
+    using wide = __int128;
     if (a.count > b.count) std::swap(a, b);
-    const wide a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
-    auto end = [](wide at, const ByteRows &r) { return at + static_cast<wide>(r.count - 1) * r.stride + r.width; };
-    if (end(a0, a) <= b0 || end(b0, b) <= a0) return false;
+    const wide a0 = a.begin, b0 = b.begin;
     auto floor_div = [](wide n, wide d) { return n / d - (n % d < 0 ? 1 : 0); };  // d > 0
     if (a.count == 1) {
         // the first row of b that ends behind a's start

@@ -1484,10 +1484,11 @@ patch_status patch_block_norm(const patch_block_norm_args *a, int64_t M, int64_t
                                      real_rows(pre.weight, 1, C, C, pre.fp32),
                                      real_rows(pre.bias, 1, C, C, pre.fp32)};
     for (int i = 0; i < 3; ++i) {
+        if (outs[i].begin == outs[i].end) continue;
         for (int j = i + 1; j < 3; ++j)
             if (patchk::overlap(outs[i], outs[j])) return PATCH_ERR_INVALID_ARG;
         for (int j = 0; j < 7; ++j) {
-            const bool in_place = i < 2 && j < 2 && outs[i].at == ins[j].at;
+            const bool in_place = i < 2 && j < 2 && outs[i].begin == ins[j].begin;
             if (!in_place && patchk::overlap(outs[i], ins[j])) return PATCH_ERR_INVALID_ARG;
         }
     }
