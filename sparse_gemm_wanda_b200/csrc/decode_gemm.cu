@@ -566,7 +566,8 @@ decode_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                 uint32_t r0[16], r1[16];
                 if (mask & 1u) tmem_ld_32x32b_x16(lane_base + (2 * buf) * BN + c0, r0);
                 if (mask & 2u) tmem_ld_32x32b_x16(lane_base + (2 * buf + 1) * BN + c0, r1);
-                tmem_ld_wait();
+                tmem_ld_wait(r0);
+                tmem_ld_wait(r1);
                 if (*abort_flag == 0) {
                     float v[16];
 #pragma unroll

@@ -345,7 +345,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 for (int c0 = c_first; c0 < m_valid; c0 += kChunkStep) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         if (c0 + q < m_valid) part[(c0 + q) * kBand] = __uint_as_float(r[q]);
@@ -376,7 +376,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 for (int c0 = c_first; c0 < m_valid; c0 += kChunkStep) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * BN + c0), r);
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         if (c0 + q < m_valid) {

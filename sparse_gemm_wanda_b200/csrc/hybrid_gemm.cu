@@ -625,7 +625,7 @@ hybrid_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             for (int c0 = c_first; c0 < (whole ? 0 : BN); c0 += kChunkStep) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(lane_base + buf * BN + c0, r);
-                tmem_ld_wait();
+                tmem_ld_wait(r);
                 if (!live) continue;
                 if (part) {
 #pragma unroll

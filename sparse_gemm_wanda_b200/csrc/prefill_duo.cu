@@ -415,7 +415,7 @@ duo_gemm_kernel(const __grid_constant__ DuoMaps maps, const __grid_constant__ Du
                 for (int c0 = 16 * grp; c0 < m_valid; c0 += 32) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(buf * bn + c0), r);
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
                     const int64_t ld = p.N[mi];
                     int64_t idx = (m_base + c0) * ld + n;
 #pragma unroll

@@ -450,7 +450,7 @@ duo_fp8_kernel(const __grid_constant__ D8Maps maps, const __grid_constant__ D8Pa
                     // token scales of the chunk: lane l holds column l % 16's
                     const int ml = c0 + (lane & 15);
                     const float sxl = ml < m_valid ? __ldg(p.sx + m_base + ml) : 0.0f;
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
                     int64_t idx = (m_base + c0) * ld + n;
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {

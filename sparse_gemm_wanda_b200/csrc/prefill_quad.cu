@@ -359,7 +359,7 @@ quad_gemm_kernel(const __grid_constant__ QuadMaps maps, const __grid_constant__ 
                 for (int c0 = 0; c0 < m_valid; c0 += 16) {
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(c0), r);
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         if (c0 + q < m_valid) store_y(p, (m_base + c0 + q) * p.N + n, __uint_as_float(r[q]));
