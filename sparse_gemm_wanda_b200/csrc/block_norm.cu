@@ -640,9 +640,9 @@ cudaError_t launch_block_norm(const BlockNormParams &p, cudaStream_t stream) {
     //   two blocks to an SM and the residual read late (2048 x 4096 13.3
     //   against 14.3 and 13.8; 4096 x 5120, two norms, 42 against 53 and 47);
     // - many bf16 rows: the streaming kernel (4096 x 4096 22.3 against 28.3,
-    //   two norms on 4096 x 5120 34.5 against 42; but 1024 x 8192 16.1 against
+    //   two norms on 4096 x 5120 35.5 against 42; but 1024 x 8192 16.1 against
     //   13.8, the rows being too few for its start), with two norms on four
-    //   chunks a thread, so more rows are under way (34.5 against 38.1).
+    //   chunks a thread, so more rows are under way (35.5 against 38.1).
     int threads, smem;
     if (vec && AllBf16::fit(p) && p.C >= 1024 && values >= 10000000) {
         if (p.post.kind != kNormNone && stream_teams<4, 768>(p, &threads, &smem) > 1)

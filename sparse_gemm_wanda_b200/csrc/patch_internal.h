@@ -166,7 +166,8 @@ struct GemmLaunch {
 // passes them on: behind its wait it raises `chain_flag` (release at device
 // scope), and a follower starts early only where it sees the flag raised
 // (acquire, and a proxy fence before its bulk copies); else it waits like any
-// other product.  The last follower lowers the flag at its end, when every
+// other product (0.1 to 0.8 us a group: 3 x 1152x512, M = 213, 13.8 -> 14.5, one
+// after another 30.0).  The last follower lowers the flag at its end, when every
 // kernel of the chain is complete.
 // A follower's epilogue waits for the kernel before it where it may share memory
 // with that (split ranges' partials, the gate's values), else only at its end,
